@@ -1,0 +1,204 @@
+// kvk_chunk_fma.cu -- CUDA-core (FFMA) attention of chunks of new tokens over a paged cache.
+//
+// Query row j of sequence i (position p = len - count + j) and head h:
+//     z_t = sigma (q_lat . c_hat_t[:d] + q_rope . c_hat_t[d:]),  t <= p
+//     out = sum_t softmax(z)_t c_hat_t[:d],   lse = log sum_t exp(z_t)
+// (the absorbed MLA attention of kvk_decode_fma.cu with a causal limit per row and the rows
+// found through the block table).  This kernel takes every shape and every query type; fp32
+// queries always take it.
+//
+// Schedule: one CTA per query token and group of 8 heads (one warp per head): the token's heads
+// share the dequantised tile of TT tokens in shared memory.  Every lane scores one token, the
+// warp runs the online softmax (base 2, fp32), lane j accumulates features j, j + 32, ...
+#include <float.h>
+
+#include "kvk_paged.cuh"
+
+namespace kvk {
+namespace {
+
+constexpr int kHG = 8;   // heads per CTA = warps per block
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float load_q(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float load_q(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float load_q(const __half* p) { return __half2float(*p); }
+__device__ __forceinline__ void store_o(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_o(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store_o(__half* p, float v) { *p = __float2half_rn(v); }
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+template <int TT, int R, typename Tq>
+__global__ void __launch_bounds__(kHG * 32) chunk_fma_kernel(const __grid_constant__ ChunkArgs a) {
+  extern __shared__ float4 smem4[];
+  float* smem = reinterpret_cast<float*>(smem4);
+  const int n = a.n, d = a.d;
+  const int ldc = n + 1;
+  float* qs = smem;                                        // [kHG][n]
+  float* cs = qs + kHG * n;                                // [TT][n + 1]
+  float* ss = cs + TT * ldc;                               // [TT]
+  int32_t* slot_s = reinterpret_cast<int32_t*>(ss + TT);   // [TT]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+  const int row = blockIdx.x, h = blockIdx.y * kHG + warp;
+  const bool hv = h < a.H;
+
+  // the sequence of this query row: the first whose rows end behind it
+  int seq = 0;
+  for (int i0 = 0; i0 < a.batch; i0 += nt) {
+    const bool before = i0 + tid < a.batch && __ldg(a.q_start + i0 + tid + 1) <= row;
+    seq += __syncthreads_count(before);
+  }
+  bool bad = false;
+  if (blockIdx.x == 0 && blockIdx.y == 0) {   // one CTA reports what had to be clamped
+    for (int i = tid; i < a.batch; i += nt) {
+      bool b1;
+      chunk_seq(a, i, &b1);
+      bad = bad || b1;
+    }
+    if (bad) atomicOr(a.flags, KVK_FLAG_SEQ_LEN);
+  }
+  if (seq >= a.batch) return;                  // a row behind the last sequence: left alone
+  const ChunkSeq s = chunk_seq(a, seq, &bad);
+  if (row < s.row0 || row >= s.row0 + s.count) return;
+  const int limit = min(s.len, max(0, s.len - s.count + (row - s.row0) + 1));   // tokens seen
+
+  const Tq* qlat = static_cast<const Tq*>(a.q_lat) + (int64_t)row * a.ql_st;
+  const Tq* qrope = static_cast<const Tq*>(a.q_rope) + (int64_t)row * a.qr_st;
+  // b = KVK_BITS_BF16: 16-bit fields holding bf16 values instead of offset-binary codes
+  const bool bf16_rows = (a.b == KVK_BITS_BF16);
+  const int b = bf16_rows ? 16 : a.b;
+  const uint32_t mask = (1u << b) - 1u;
+  const int zero_off = 1 << (b - 1);
+  const float zscale = a.sigma * kLog2e;
+  for (int k = lane; k < n; k += 32) {
+    float v = 0.0f;
+    if (hv)
+      v = (k < d) ? load_q(qlat + (int64_t)h * a.ql_sh + k)
+                  : load_q(qrope + (int64_t)h * a.qr_sh + (k - d));
+    qs[warp * n + k] = v;
+  }
+  float m = -INFINITY, l = 0.0f;
+  float o[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) o[r] = 0.0f;
+
+  for (int p = 0; p < limit; p += TT) {
+    const int cnt = min(TT, limit - p);
+    __syncthreads();
+    if (tid < TT) {
+      const int t = (tid < cnt) ? chunk_slot(a, seq, p + tid) : -1;
+      slot_s[tid] = t;
+      // a group-scaled cache carries its scales per element (below): unit token scale
+      ss[tid] = (t >= 0) ? (a.group ? 1.0f : __half2float(a.scales[t])) : 0.0f;
+    }
+    __syncthreads();
+    for (int e = tid; e < TT * n; e += nt) {
+      const int i = e / n, k = e - i * n;
+      const int t = slot_s[i];
+      float v = 0.0f;
+      if (t >= 0) {
+        const uint32_t* crow =
+            reinterpret_cast<const uint32_t*>(a.codes + (int64_t)t * a.row_bytes);
+        const int bit = k * b;
+        const uint32_t w = __ldg(crow + (bit >> 5));
+        const uint32_t u = (w >> (bit & 31)) & mask;
+        v = bf16_rows ? __uint_as_float(u << 16) : (float)((int)u - zero_off);
+        if (a.group) v *= __half2float(a.scales[(int64_t)t * a.sg + k / a.group]);
+      }
+      cs[i * ldc + k] = v;
+    }
+    __syncthreads();
+    float z2 = -INFINITY;
+    if (hv && lane < cnt && slot_s[lane] >= 0) {
+      float acc = 0.0f;
+      const float* qr = qs + warp * n;
+      const float* cr = cs + lane * ldc;
+      for (int k = 0; k < n; ++k) acc = fmaf(qr[k], cr[k], acc);
+      z2 = acc * ss[lane] * zscale;
+    }
+    const float mn = fmaxf(m, warp_max(z2));
+    const float alpha = (m == -INFINITY || mn == -INFINITY) ? 0.0f : exp2f(m - mn);
+    const float pz = (z2 == -INFINITY) ? 0.0f : exp2f(z2 - mn);
+    l = l * alpha + warp_sum(pz);
+    const float wgt = pz * ss[lane];
+#pragma unroll
+    for (int r = 0; r < R; ++r) o[r] *= alpha;
+    for (int i = 0; i < cnt; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, wgt, i);
+      const float* cr = cs + i * ldc;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int j = lane + 32 * r;
+        if (j < d) o[r] = fmaf(wi, cr[j], o[r]);
+      }
+    }
+    m = mn;
+  }
+  if (!hv) return;
+  const float inv = (l > 0.0f || l != l) ? 1.0f / l : 0.0f;
+  Tq* out = static_cast<Tq*>(a.out) + (int64_t)row * a.o_st + (int64_t)h * a.o_sh;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int j = lane + 32 * r;
+    if (j < d) store_o(out + j, o[r] * inv);
+  }
+  if (a.lse && lane == 0)
+    a.lse[(int64_t)row * a.H + h] = (l == 0.0f) ? -INFINITY : kLn2 * (m + log2f(l));
+}
+
+template <int TT, int R>
+cudaError_t launch_tt_r(const ChunkArgs& a, int dtype, size_t smem, cudaStream_t st) {
+  dim3 grid((unsigned)a.n_q, (unsigned)((a.H + kHG - 1) / kHG)), block(kHG * 32);
+  cudaError_t e = cudaSuccess;
+#define KVK_LAUNCH(T)                                                                   \
+  do {                                                                                  \
+    auto k = chunk_fma_kernel<TT, R, T>;                                                \
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); \
+    if (e != cudaSuccess) return e;                                                     \
+    k<<<grid, block, smem, st>>>(a);                                                    \
+  } while (0)
+  if (dtype == KVK_F32) KVK_LAUNCH(float);
+  else if (dtype == KVK_BF16) KVK_LAUNCH(__nv_bfloat16);
+  else KVK_LAUNCH(__half);
+#undef KVK_LAUNCH
+  return cudaGetLastError();
+}
+
+template <int TT>
+cudaError_t launch_tt(const ChunkArgs& a, int dtype, size_t smem, cudaStream_t st) {
+  if (a.d <= 64) return launch_tt_r<TT, 2>(a, dtype, smem, st);
+  if (a.d <= 128) return launch_tt_r<TT, 4>(a, dtype, smem, st);
+  if (a.d <= 512) return launch_tt_r<TT, 16>(a, dtype, smem, st);
+  return launch_tt_r<TT, 64>(a, dtype, smem, st);
+}
+
+constexpr size_t kSmemMax = 227 * 1024;
+
+size_t smem_bytes(int TT, int n) {
+  return sizeof(float) * ((size_t)kHG * n + (size_t)TT * (n + 1) + TT) + sizeof(int32_t) * (size_t)TT;
+}
+
+}  // namespace
+
+bool chunk_fma_fits(int n) { return smem_bytes(16, n) <= kSmemMax; }
+
+cudaError_t launch_chunk_fma(const ChunkArgs& a, int dtype, cudaStream_t st) {
+  const size_t s32 = smem_bytes(32, a.n);
+  if (s32 <= kSmemMax) return launch_tt<32>(a, dtype, s32, st);
+  const size_t s16 = smem_bytes(16, a.n);
+  if (s16 <= kSmemMax) return launch_tt<16>(a, dtype, s16, st);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace kvk

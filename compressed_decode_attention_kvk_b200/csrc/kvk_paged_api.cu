@@ -1,0 +1,214 @@
+// kvk_paged_api.cu -- host side of the paged entry points: argument checks and dispatch.  Every
+// exported symbol is declared in include/kvk.h.
+#include <string.h>
+
+#include <algorithm>
+
+#include "kvk_paged.cuh"
+
+using kvk::AnchorDesc;
+
+namespace {
+
+bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// As for every call of a layout: its device has to be the current one.
+kvk_status check_device(const kvk_layout* L) {
+  int cur = -1;
+  if (cudaGetDevice(&cur) != cudaSuccess) {
+    cudaGetLastError();
+    return KVK_ERR_CUDA;
+  }
+  return cur == L->device ? KVK_OK : KVK_ERR_INVALID_ARG;
+}
+
+// Tokens per page: a power of two up to 2^16.  Returns its logarithm, or -1.
+int page_shift(int page_tokens) {
+  if (page_tokens < 1 || page_tokens > 65536 || (page_tokens & (page_tokens - 1))) return -1;
+  int s = 0;
+  while ((1 << s) < page_tokens) ++s;
+  return s;
+}
+
+int64_t pool_slots(const kvk_layout* L) { return (int64_t)L->max_batch * L->max_tokens; }
+
+// The kernel a chunk call takes, or -1.
+int chunk_path(const kvk_layout* L, const AnchorDesc& A, int dtype) {
+  (void)dtype;
+  if (L->path == KVK_PATH_TENSOR || L->path == KVK_PATH_TENSOR_GENERAL) return -1;
+  return kvk::chunk_fma_fits(A.n) ? KVK_PATH_CUDA_CORE : -1;
+}
+
+bool known_dtype(int t) { return t == KVK_F32 || t == KVK_BF16 || t == KVK_F16; }
+
+}  // namespace
+
+extern "C" {
+
+kvk_status kvk_paged_plan(kvk_layout* L, const int32_t* dev_cached, const int32_t* dev_new,
+                          int batch, const int32_t* dev_free_pages, const int32_t* dev_free_count,
+                          int free_capacity, int page_tokens, int32_t* dev_block_table,
+                          int table_pages, int64_t table_stride, int max_new,
+                          int32_t* dev_seq_lens, int32_t* dev_q_start, int32_t* dev_slots,
+                          int32_t* dev_positions, int32_t* dev_free_count_out,
+                          kvk_stream_t stream) {
+  if (!L || !L->arena) return KVK_ERR_INVALID_ARG;
+  if (batch < 1 || batch > kvk::kMaxPagedBatch || free_capacity < 0 || table_pages < 1 ||
+      table_stride < table_pages || max_new < 0)
+    return KVK_ERR_INVALID_ARG;
+  const int shift = page_shift(page_tokens);
+  if (shift < 0) return KVK_ERR_INVALID_ARG;
+  if (!dev_cached || !dev_new || !dev_free_count || !dev_block_table || !dev_seq_lens ||
+      !dev_q_start || !dev_free_count_out || (free_capacity > 0 && !dev_free_pages) ||
+      (max_new > 0 && !dev_slots))
+    return KVK_ERR_INVALID_ARG;
+  // the lengths are read while the results are written
+  if (dev_seq_lens == dev_cached || dev_seq_lens == dev_new || dev_q_start == dev_cached ||
+      dev_q_start == dev_new)
+    return KVK_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)dev_cached, (const void*)dev_new, (const void*)dev_free_pages,
+                        (const void*)dev_free_count, (const void*)dev_block_table,
+                        (const void*)dev_seq_lens, (const void*)dev_q_start,
+                        (const void*)dev_slots, (const void*)dev_positions,
+                        (const void*)dev_free_count_out})
+    if (!aligned(p, 4)) return KVK_ERR_ALIGNMENT;
+  if (kvk_status ds = check_device(L)) return ds;
+  kvk::PlanArgs a;
+  memset(&a, 0, sizeof(a));
+  a.cached = dev_cached;
+  a.fresh = dev_new;
+  a.batch = batch;
+  a.free_pages = dev_free_pages;
+  a.free_count = dev_free_count;
+  a.free_capacity = free_capacity;
+  a.page_shift = shift;
+  a.pool_pages = (int)(pool_slots(L) >> shift);
+  a.table = dev_block_table;
+  a.table_pages = table_pages;
+  a.table_stride = table_stride;
+  a.max_new = max_new;
+  a.seq_lens = dev_seq_lens;
+  a.q_start = dev_q_start;
+  a.slots = dev_slots;
+  a.positions = dev_positions;
+  a.free_count_out = dev_free_count_out;
+  a.flags = reinterpret_cast<uint32_t*>(L->arena);
+  const cudaError_t e = kvk::launch_paged_plan(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVK_OK : KVK_ERR_CUDA;
+}
+
+kvk_status kvk_paged_write(kvk_layout* L, int layer, const void* c_kv, int dtype,
+                           int64_t c_stride_tok, const void* k_rope, int64_t kr_stride_tok,
+                           int n_tokens, const int32_t* dev_slots, kvk_stream_t stream) {
+  if (!L || layer < 0 || layer >= L->n_layers) return KVK_ERR_INVALID_ARG;
+  if (L->anchor[layer] != layer) return KVK_ERR_INHERITING_LAYER;
+  if (!L->arena) return KVK_ERR_INVALID_ARG;
+  if (dtype != KVK_F32 && dtype != KVK_BF16) return KVK_ERR_INVALID_ARG;
+  if (n_tokens < 0) return KVK_ERR_INVALID_ARG;
+  if (n_tokens == 0) return KVK_OK;
+  if (!c_kv || !dev_slots || (L->d_rope > 0 && !k_rope)) return KVK_ERR_INVALID_ARG;
+  if (c_stride_tok < 0 || kr_stride_tok < 0) return KVK_ERR_INVALID_ARG;
+  if (!aligned(c_kv, 16) || !aligned(k_rope, 16) || !aligned(dev_slots, 4) || c_stride_tok % 8 ||
+      kr_stride_tok % 8)
+    return KVK_ERR_ALIGNMENT;
+  if (kvk_status ds = check_device(L)) return ds;
+  const AnchorDesc& A = L->anchors[L->slot[layer]];
+  const cudaError_t e =
+      kvk::launch_paged_write(L, A, c_kv, dtype, c_stride_tok, k_rope, kr_stride_tok, n_tokens,
+                              dev_slots, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVK_OK : KVK_ERR_CUDA;
+}
+
+kvk_status kvk_chunk_path_for(const kvk_layout* L, int layer, int dtype, int* path) {
+  if (!L || !path || layer < 0 || layer >= L->n_layers || !known_dtype(dtype))
+    return KVK_ERR_INVALID_ARG;
+  const int p = chunk_path(L, L->anchors[L->slot[layer]], dtype);
+  if (p < 0) return KVK_ERR_UNSUPPORTED;
+  *path = p;
+  return KVK_OK;
+}
+
+kvk_status kvk_chunk_workspace_bytes(const kvk_layout* L, int layer, int n_q, int batch,
+                                     int n_heads, size_t* bytes) {
+  if (!L || !bytes || layer < 0 || layer >= L->n_layers || n_q < 0 || batch < 1 ||
+      batch > kvk::kMaxPagedBatch || n_heads < 1 || n_heads > 4096)
+    return KVK_ERR_INVALID_ARG;
+  *bytes = 256;   // the CUDA-core kernel needs none
+  return KVK_OK;
+}
+
+kvk_status kvk_mla_chunk(kvk_layout* L, int layer, const void* q_lat, const void* q_rope,
+                         int dtype, int64_t q_lat_stride_tok, int64_t q_lat_stride_head,
+                         int64_t q_rope_stride_tok, int64_t q_rope_stride_head, int n_q, int batch,
+                         int n_heads, const int32_t* dev_q_start, const int32_t* dev_seq_lens,
+                         const int32_t* dev_block_table, int table_pages, int64_t table_stride,
+                         int page_tokens, float softmax_scale, void* out, int64_t out_stride_tok,
+                         int64_t out_stride_head, float* lse, void* workspace,
+                         size_t workspace_bytes, kvk_stream_t stream) {
+  if (!L || layer < 0 || layer >= L->n_layers || !L->arena) return KVK_ERR_INVALID_ARG;
+  if (!known_dtype(dtype)) return KVK_ERR_INVALID_ARG;
+  if (n_q < 0 || batch < 1 || batch > kvk::kMaxPagedBatch || n_heads < 1 || n_heads > 4096 ||
+      (int64_t)n_q * n_heads >= (int64_t)1 << 31)
+    return KVK_ERR_INVALID_ARG;
+  const int shift = page_shift(page_tokens);
+  if (shift < 0 || table_pages < 1 || table_stride < table_pages) return KVK_ERR_INVALID_ARG;
+  if (n_q == 0) return KVK_OK;
+  if (!q_lat || (L->d_rope > 0 && !q_rope) || !dev_q_start || !dev_seq_lens || !dev_block_table ||
+      !out || !workspace)
+    return KVK_ERR_INVALID_ARG;
+  for (int64_t s : {q_lat_stride_tok, q_lat_stride_head, q_rope_stride_tok, q_rope_stride_head,
+                    out_stride_tok, out_stride_head}) {
+    if (s < 0) return KVK_ERR_INVALID_ARG;
+    if (s % 8) return KVK_ERR_ALIGNMENT;
+  }
+  for (const void* p : {(const void*)q_lat, (const void*)q_rope, (const void*)out,
+                        (const void*)lse, (const void*)workspace})
+    if (!aligned(p, 16)) return KVK_ERR_ALIGNMENT;
+  for (const int32_t* p : {dev_q_start, dev_seq_lens, dev_block_table})
+    if (!aligned(p, 4)) return KVK_ERR_ALIGNMENT;
+  if (kvk_status ds = check_device(L)) return ds;
+  const AnchorDesc& A = L->anchors[L->slot[layer]];
+  const int path = chunk_path(L, A, dtype);
+  if (path < 0) return KVK_ERR_UNSUPPORTED;
+
+  kvk::ChunkArgs a;
+  memset(&a, 0, sizeof(a));
+  a.codes = L->arena + A.codes_off;
+  a.scales = reinterpret_cast<const __half*>(L->arena + A.scales_off);
+  a.row_bytes = A.row_bytes;
+  a.d = A.d;
+  a.d_rope = L->d_rope;
+  a.n = A.n;
+  a.b = A.b;
+  a.group = kvk::anchor_group(L, A);
+  a.sg = A.sg;
+  a.q_lat = q_lat;
+  a.q_rope = q_rope;
+  a.ql_st = q_lat_stride_tok;
+  a.ql_sh = q_lat_stride_head;
+  a.qr_st = q_rope_stride_tok;
+  a.qr_sh = q_rope_stride_head;
+  a.n_q = n_q;
+  a.batch = batch;
+  a.H = n_heads;
+  a.q_start = dev_q_start;
+  a.seq_lens = dev_seq_lens;
+  a.table = dev_block_table;
+  a.table_pages = table_pages;
+  a.table_stride = table_stride;
+  a.page_shift = shift;
+  a.pool_pages = (int)(pool_slots(L) >> shift);
+  a.cap = (int)std::min<int64_t>((int64_t)table_pages << shift, (int64_t)1 << 30);
+  a.sigma = softmax_scale;
+  a.out = out;
+  a.o_st = out_stride_tok;
+  a.o_sh = out_stride_head;
+  a.lse = lse;
+  a.flags = reinterpret_cast<uint32_t*>(L->arena);
+  a.limit_ns = L->wait_limit_ns ? L->wait_limit_ns : kvk::kDefaultWaitLimitNs;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = kvk::launch_chunk_fma(a, dtype, st);
+  return e == cudaSuccess ? KVK_OK : KVK_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -24,7 +25,7 @@ STATUS_NAMES = {0: "KVK_OK", 1: "KVK_ERR_INVALID_ARG", 2: "KVK_ERR_BAD_TABLE",
 KVK_F32, KVK_BF16, KVK_F16 = 0, 1, 2
 KVK_PATH_AUTO, KVK_PATH_TENSOR, KVK_PATH_CUDA_CORE, KVK_PATH_TENSOR_GENERAL = 0, 1, 2, 3
 KVK_FLAG_NONFINITE, KVK_FLAG_WRITE_RANGE, KVK_FLAG_SEQ_LEN, KVK_FLAG_KEEP_INDEX = 1, 2, 4, 8
-KVK_FLAG_TIMEOUT = 16
+KVK_FLAG_TIMEOUT, KVK_FLAG_PAGE = 16, 32
 
 _DTYPE = {torch.float32: KVK_F32, torch.bfloat16: KVK_BF16, torch.float16: KVK_F16}
 
@@ -34,7 +35,8 @@ EXPORTED = ("kvk_create_layout", "kvk_destroy", "kvk_get_layer_info", "kvk_quant
             "kvk_set_decode_path", "kvk_set_decode_ctas", "kvk_decode_path_for",
             "kvk_status_string", "kvk_mla_decode_noalloc", "kvk_quant_write_layers",
             "kvk_decode_workspace_bytes_keep", "kvk_set_wait_limit", "kvk_mla_decode_append",
-            "kvk_create_layout_grouped", "kvk_absorb")
+            "kvk_create_layout_grouped", "kvk_absorb", "kvk_paged_plan", "kvk_paged_write",
+            "kvk_mla_chunk", "kvk_chunk_workspace_bytes", "kvk_chunk_path_for")
 
 # size of the library's built-in scratch array used by kvk_mla_decode_noalloc
 KVK_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -72,6 +74,13 @@ def _lib_handle():
                                                 sz, P, P, P]
         L.kvk_absorb.argtypes = [P, i32, i64, i64, P, i64, i64, P, i32, i64, i64, i32, i32, i32,
                                  i32, P]
+        L.kvk_paged_plan.argtypes = [P, P, P, i32, P, P, i32, i32, P, i32, i64, i32, P, P, P, P,
+                                     P, P]
+        L.kvk_paged_write.argtypes = [P, i32, P, i32, i64, P, i64, i32, P, P]
+        L.kvk_mla_chunk.argtypes = [P, i32, P, P, i32, i64, i64, i64, i64, i32, i32, i32, P, P, P,
+                                    i32, i64, i32, ctypes.c_float, P, i64, i64, P, P, sz, P]
+        L.kvk_chunk_workspace_bytes.argtypes = [P, i32, i32, i32, i32, P]
+        L.kvk_chunk_path_for.argtypes = [P, i32, i32, P]
         L.kvk_destroy.argtypes = [P]
         L.kvk_destroy.restype = None
         L.kvk_get_layer_info.argtypes = [P, i32, P]
@@ -116,6 +125,20 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _row_stride(t, dim=0):
+    """Stride of a dim; of one that has a single entry (whose stride torch leaves open) the
+    packed one, and of a tensor without elements (no RoPE part) zero, so that they do not meet
+    the library's alignment checks."""
+    if t.numel() == 0:
+        return 0
+    if t.shape[dim] > 1:
+        return t.stride(dim)
+    inner = 1
+    for k in range(dim + 1, t.dim()):
+        inner = max(inner, t.shape[k] * t.stride(k)) if t.shape[k] > 1 else max(inner, t.shape[k])
+    return (inner + 7) // 8 * 8
 
 
 def _need_cuda(t, name, dtypes=None):
@@ -329,6 +352,106 @@ def kvk_absorb(x, w, y, stream=None):
     return y
 
 
+def kvk_paged_plan(handle, cached, new, free_pages, free_count, block_table, page_tokens, max_new,
+                   seq_lens, q_start, slots, positions, free_count_out, stream=None):
+    """The pages and slots of a step's new tokens.  cached, new int32 [B]; free_pages int32 [F]
+    with free_count int32 [1] valid entries; block_table int32 [B, pages] (updated in place);
+    results: seq_lens int32 [B], q_start int32 [B + 1], slots and positions (or None) int32
+    [>= max_new], free_count_out int32 [1] (may be free_count)."""
+    for t, name in ((cached, "cached"), (new, "new"), (free_pages, "free_pages"),
+                    (free_count, "free_count"), (block_table, "block_table"),
+                    (seq_lens, "seq_lens"), (q_start, "q_start"), (slots, "slots"),
+                    (positions, "positions"), (free_count_out, "free_count_out")):
+        _need_cuda(t, name, (torch.int32,))
+        if t is not None and name != "block_table" and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if block_table.dim() != 2 or block_table.stride(1) != 1:
+        raise ValueError("block_table must be [batch, pages] with contiguous rows")
+    B = cached.numel()
+    if new.numel() != B or block_table.shape[0] != B or seq_lens.numel() < B or \
+            q_start.numel() < B + 1 or slots.numel() < max_new or \
+            (positions is not None and positions.numel() < max_new) or \
+            free_count.numel() < 1 or free_count_out.numel() < 1:
+        raise ValueError("sizes of the plan's tensors do not match the batch and max_new")
+    st = _lib_handle().kvk_paged_plan(
+        handle, _ptr(cached), _ptr(new), B, _ptr(free_pages), _ptr(free_count),
+        free_pages.numel(), page_tokens, _ptr(block_table), block_table.shape[1],
+        _row_stride(block_table), max_new, _ptr(seq_lens), _ptr(q_start), _ptr(slots),
+        _ptr(positions), _ptr(free_count_out), _stream(stream))
+    _check("kvk_paged_plan", st)
+
+
+def kvk_paged_write(handle, layer, c_kv, k_rope, slots, stream=None):
+    """c_kv [N, >=d], k_rope [N, d_rope] (fp32 or bf16, CUDA, last dim contiguous) quantised to
+    slots int32 [>= N] of the layer's pool (negative: skipped)."""
+    _need_cuda(c_kv, "c_kv", (torch.float32, torch.bfloat16))
+    _need_cuda(k_rope, "k_rope", (c_kv.dtype,))
+    _need_cuda(slots, "slots", (torch.int32,))
+    if c_kv.dim() != 2 or k_rope.dim() != 2 or \
+            any(t.shape[1] > 1 and t.stride(1) != 1 for t in (c_kv, k_rope)):
+        raise ValueError("c_kv / k_rope must be [tokens, width] with contiguous width")
+    if k_rope.shape[0] != c_kv.shape[0] or slots.numel() < c_kv.shape[0] or \
+            not slots.is_contiguous():
+        raise ValueError("k_rope and slots must cover c_kv's tokens")
+    st = _lib_handle().kvk_paged_write(handle, layer, _ptr(c_kv), _DTYPE[c_kv.dtype],
+                                       _row_stride(c_kv), _ptr(k_rope), _row_stride(k_rope),
+                                       c_kv.shape[0], _ptr(slots), _stream(stream))
+    _check("kvk_paged_write", st)
+
+
+def kvk_mla_chunk(handle, layer, q_lat, q_rope, q_start, seq_lens, block_table, page_tokens,
+                  softmax_scale, out, workspace, lse=None, stream=None):
+    """Causal attention of packed query rows over the paged cache.  q_lat [N, H, >=d], q_rope
+    [N, H, d_rope] (same dtype, CUDA, last dim contiguous); q_start int32 [B + 1], seq_lens int32
+    [B], block_table int32 [B, pages]; out [N, H, >=d] of the queries' dtype (last dim
+    contiguous); lse fp32 [N, H] (optional); workspace uint8 CUDA tensor."""
+    _need_cuda(q_lat, "q_lat", tuple(_DTYPE))
+    _need_cuda(q_rope, "q_rope", (q_lat.dtype,))
+    _need_cuda(out, "out", (q_lat.dtype,))
+    _need_cuda(lse, "lse", (torch.float32,))
+    _need_cuda(workspace, "workspace")
+    for t, name in ((q_start, "q_start"), (seq_lens, "seq_lens"), (block_table, "block_table")):
+        _need_cuda(t, name, (torch.int32,))
+    if any(t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) for t in (q_lat, q_rope, out)):
+        raise ValueError("q_lat, q_rope and out must be [rows, heads, width] with contiguous width")
+    if block_table.dim() != 2 or block_table.stride(1) != 1:
+        raise ValueError("block_table must be [batch, pages] with contiguous rows")
+    if lse is not None and not lse.is_contiguous():
+        raise ValueError("lse must be contiguous")
+    N, H = q_lat.shape[0], q_lat.shape[1]
+    B = seq_lens.numel()
+    if q_rope.shape[:2] != (N, H) or out.shape[:2] != (N, H) or q_start.numel() < B + 1 or \
+            block_table.shape[0] != B or not q_start.is_contiguous() or \
+            not seq_lens.is_contiguous() or (lse is not None and tuple(lse.shape) != (N, H)):
+        raise ValueError("shapes of the queries, outputs, lengths and block table do not match")
+    info = kvk_get_layer_info(handle, layer)
+    if q_lat.shape[2] < info["d"] or out.shape[2] < info["d"] or q_rope.shape[2] < info["d_rope"]:
+        raise ValueError("q_lat, q_rope or out is narrower than the layer's rows")
+    st = _lib_handle().kvk_mla_chunk(
+        handle, layer, _ptr(q_lat), _ptr(q_rope), _DTYPE[q_lat.dtype], _row_stride(q_lat),
+        _row_stride(q_lat, 1), _row_stride(q_rope), _row_stride(q_rope, 1), N, B, H,
+        _ptr(q_start), _ptr(seq_lens), _ptr(block_table), block_table.shape[1],
+        _row_stride(block_table), page_tokens, float(softmax_scale), _ptr(out), _row_stride(out),
+        _row_stride(out, 1), _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("kvk_mla_chunk", st)
+
+
+def kvk_chunk_workspace_bytes(handle, layer, n_q, batch, n_heads) -> int:
+    out = ctypes.c_size_t(0)
+    _check("kvk_chunk_workspace_bytes",
+           _lib_handle().kvk_chunk_workspace_bytes(handle, layer, n_q, batch, n_heads,
+                                                   ctypes.byref(out)))
+    return out.value
+
+
+def kvk_chunk_path_for(handle, layer, dtype) -> int:
+    p = ctypes.c_int(0)
+    _check("kvk_chunk_path_for", _lib_handle().kvk_chunk_path_for(
+        handle, layer, _DTYPE.get(dtype, dtype), ctypes.byref(p)))
+    return p.value
+
+
 def kvk_read_status(handle, clear=False, stream=None) -> int:
     v = ctypes.c_uint32(0)
     _check("kvk_read_status", _lib_handle().kvk_read_status(handle, ctypes.byref(v),
@@ -362,6 +485,15 @@ def kvk_status_string(status) -> str:
 # ---------------------------------------------------------------------------
 # convenience wrapper
 # ---------------------------------------------------------------------------
+
+class PagedPlan(NamedTuple):
+    """A paged step's bookkeeping (Layout.paged_plan): int32 CUDA tensors."""
+    seq_lens: torch.Tensor      # [B] tokens in the cache, the new ones among them
+    q_start: torch.Tensor       # [B + 1] first packed row of each sequence
+    slots: torch.Tensor         # [max_new] slot of each new token (-1 behind the last)
+    positions: torch.Tensor     # [max_new] position in its sequence
+    free_count: torch.Tensor    # [1] pages left in the free list
+
 
 class Layout:
     """A per-layer plan plus its arena (a CUDA uint8 tensor owned by this object unless
@@ -456,6 +588,51 @@ class Layout:
         kvk_mla_decode_append(self.handle, layer, c_new, k_rope_new, q_lat, q_rope, seq_lens,
                               softmax_scale, out, workspace, lse=lse, stream=stream)
         return out
+
+    def new_paged_plan(self, batch, max_new):
+        i32 = dict(dtype=torch.int32, device=self.arena.device)
+        return PagedPlan(torch.empty(batch, **i32), torch.empty(batch + 1, **i32),
+                         torch.empty(max_new, **i32), torch.empty(max_new, **i32),
+                         torch.empty(1, **i32))
+
+    def paged_plan(self, cached, new, free_pages, free_count, block_table, page_tokens, max_new,
+                   out=None, stream=None):
+        """The pages and slots of a step's new tokens (kvk_paged_plan): block_table is updated in
+        place, free_pages[:free_count] is the free list, max_new bounds the new tokens of the
+        batch.  Returns a PagedPlan (out, if one is given)."""
+        if out is None:
+            out = self.new_paged_plan(cached.numel(), max_new)
+        kvk_paged_plan(self.handle, cached, new, free_pages, free_count, block_table, page_tokens,
+                       max_new, out.seq_lens, out.q_start, out.slots, out.positions,
+                       out.free_count, stream=stream)
+        return out
+
+    def paged_write(self, layer, c_kv, k_rope, slots, stream=None):
+        kvk_paged_write(self.handle, layer, c_kv, k_rope, slots, stream=stream)
+
+    def chunk_workspace_bytes(self, layer, n_q, batch, n_heads):
+        return kvk_chunk_workspace_bytes(self.handle, layer, n_q, batch, n_heads)
+
+    def new_chunk_workspace(self, layer, n_q, batch, n_heads):
+        return torch.empty(self.chunk_workspace_bytes(layer, n_q, batch, n_heads),
+                           dtype=torch.uint8, device=self.arena.device)
+
+    def mla_chunk(self, layer, q_lat, q_rope, q_start, seq_lens, block_table, page_tokens,
+                  softmax_scale, out=None, lse=None, workspace=None, stream=None):
+        """Causal attention of packed query rows over the paged cache (kvk_mla_chunk); returns
+        out [N, H, d] of the queries' dtype."""
+        N, H = q_lat.shape[0], q_lat.shape[1]
+        if out is None:
+            out = torch.empty(N, H, self.layer_info(layer)["d"], dtype=q_lat.dtype,
+                              device=q_lat.device)
+        if workspace is None:
+            workspace = self.new_chunk_workspace(layer, N, seq_lens.numel(), H)
+        kvk_mla_chunk(self.handle, layer, q_lat, q_rope, q_start, seq_lens, block_table,
+                      page_tokens, softmax_scale, out, workspace, lse=lse, stream=stream)
+        return out
+
+    def chunk_path_for(self, layer, dtype):
+        return kvk_chunk_path_for(self.handle, layer, dtype)
 
     def read_status(self, clear=False, stream=None):
         return kvk_read_status(self.handle, clear, stream)

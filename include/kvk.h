@@ -64,6 +64,8 @@ typedef enum { KVK_F32 = 0, KVK_BF16 = 1, KVK_F16 = 2 } kvk_dtype;
 #define KVK_FLAG_KEEP_INDEX  0x8u /* decode: keep index outside [0, seq_len); entry skipped        */
 #define KVK_FLAG_TIMEOUT     0x10u /* decode: a tensor-core kernel wait exceeded its time limit and
                                       the kernel stopped early; that call's outputs are unspecified */
+#define KVK_FLAG_PAGE        0x20u /* paged calls: the free list ran short, or a page id outside the
+                                      pool; the tokens of that page have no slot / are skipped   */
 
 /* Bit width of an anchor that keeps its cache uncompressed: rows of bfloat16 values (16 bits
  * per element, no quantisation and no scale) -- the bf16 MLA cache the compressed choices are
@@ -367,6 +369,122 @@ kvk_status kvk_absorb(const void* x, int x_dtype, int64_t x_stride_seq, int64_t 
                       const void* w, int64_t w_stride_row, int64_t w_stride_head, void* y,
                       int y_dtype, int64_t y_stride_seq, int64_t y_stride_head, int batch,
                       int n_heads, int K, int n, kvk_stream_t stream);
+
+/*
+ * The paged cache.  The planes of a layout are also a pool of max_batch * max_tokens token slots
+ * per anchor, in pages of page_tokens slots: page p holds the slots [p * page_tokens,
+ * (p + 1) * page_tokens), slot s is row s of the codes plane (and scale s, or its group scales)
+ * counted over the whole plane.  Sequences then share the pool: position t of sequence i lives
+ * in slot block_table[i][t / page_tokens] * page_tokens + t % page_tokens, the same for every
+ * layer.  A layout for paged use has any max_batch and max_tokens with that product (for example
+ * 1 x slots); a pool is used either through these calls or through the contiguous ones.
+ *   page_tokens    a power of two, 1 to 65536
+ *   batch          1 <= batch <= 4096, whatever the layout's max_batch
+ *   block table    device int32 [batch][table_pages], rows table_stride entries apart
+ */
+
+/*
+ * kvk_paged_plan -- the bookkeeping of one serving step, from the requests' lengths, in one
+ * launch: which pages the new tokens take, and where every new token goes.
+ *
+ * With a_i = dev_cached[i] tokens in the cache and f_i = dev_new[i] new ones, sequence i holds
+ * ceil(a_i / page_tokens) pages (the first entries of its table row) and gets the pages that
+ * a_i + f_i tokens need beyond them, in sequence order off the end of the free list: the k-th
+ * page taken by the batch is dev_free_pages[count - 1 - k], count = *dev_free_count.
+ *
+ *   dev_free_pages   device int32 [free_capacity], page ids; count is clamped to free_capacity
+ *   dev_block_table  the taken pages are written to the row's entries behind the held ones; no
+ *                    other entry changes
+ *   dev_seq_lens     out, int32 [batch]: a_i + f_i
+ *   dev_q_start      out, int32 [batch + 1]: exclusive prefix sums of the f_i
+ *   dev_slots        out, int32 [max_new]: the slot of each new token, the sequences' tokens end
+ *                    to end; entries behind the last token are -1
+ *   dev_positions    nullable out, int32 [max_new]: its position in its sequence (0 behind the
+ *                    last token)
+ *   dev_free_count_out  out, int32: count less the pages taken (0 at least); may be dev_free_count
+ * dev_seq_lens and dev_q_start must not overlap the inputs.
+ *
+ * Negative lengths count as 0, tokens that do not fit the table row or max_new get no slot
+ * (KVK_FLAG_SEQ_LEN).  A page that the free list cannot give, or an id outside the pool, leaves
+ * the entry at -1 and its tokens without slot (-1; KVK_FLAG_PAGE).
+ */
+kvk_status kvk_paged_plan(kvk_layout* layout, const int32_t* dev_cached, const int32_t* dev_new,
+                          int batch, const int32_t* dev_free_pages, const int32_t* dev_free_count,
+                          int free_capacity, int page_tokens, int32_t* dev_block_table,
+                          int table_pages, int64_t table_stride, int max_new,
+                          int32_t* dev_seq_lens, int32_t* dev_q_start, int32_t* dev_slots,
+                          int32_t* dev_positions, int32_t* dev_free_count_out,
+                          kvk_stream_t stream);
+
+/*
+ * kvk_paged_write -- kvk_quant_write of packed rows through a slot map: token j (0 <= j <
+ * n_tokens) is quantised as kvk_quant_write quantises it and stored in slot dev_slots[j] of the
+ * layer's pool.
+ *
+ *   layer       an anchor layer (an inheriting layer -> KVK_ERR_INHERITING_LAYER)
+ *   c_kv        device, element (j, k) at c_kv[j * c_stride_tok + k], k < d; KVK_F32 or KVK_BF16
+ *   k_rope      device, element (j, k) at k_rope[j * kr_stride_tok + k], k < d_rope; same dtype.
+ *               Strides in elements, multiples of 8.
+ *   dev_slots   device int32 [n_tokens] (kvk_paged_plan's).  A negative slot skips the token; one
+ *               outside the pool skips it and sets KVK_FLAG_WRITE_RANGE.  Two tokens of one call
+ *               must not share a slot (its row is unspecified then).
+ * Non-finite input sets KVK_FLAG_NONFINITE as in kvk_quant_write.
+ */
+kvk_status kvk_paged_write(kvk_layout* layout, int layer, const void* c_kv, int dtype,
+                           int64_t c_stride_tok, const void* k_rope, int64_t kr_stride_tok,
+                           int n_tokens, const int32_t* dev_slots, kvk_stream_t stream);
+
+/*
+ * kvk_mla_chunk -- causal attention of every sequence's new tokens over its paged cache, for one
+ * layer: a prompt's chunk, the tokens of a speculative step, or one token per sequence (a decode
+ * step), mixed in one batch.
+ *
+ * The packed query rows dev_q_start[i] .. dev_q_start[i + 1] - 1 are the last tokens of sequence
+ * i, whose dev_seq_lens[i] tokens (the new ones among them) are in the cache already.  Row j of
+ * its q_i rows sits at position dev_seq_lens[i] - q_i + j and sees every position up to its own:
+ *     z_t = softmax_scale * (q_lat . c_hat_t[0..d) + q_rope . c_hat_t[d..d+d_rope))
+ *     out = sum_t softmax(z)_t * c_hat_t[0..d),   lse = log sum_t exp(z_t)
+ * per head, as kvk_mla_decode.  A row that sees no token (its position is negative, or the pages
+ * of all of them are missing) gets out = 0 and lse = -inf.  Rows behind the last sequence are not
+ * touched.
+ *
+ *   layer        any layer; an inheriting layer reads its anchor's pool
+ *   q_lat        device, element (row, head, k) at q_lat[row * q_lat_stride_tok +
+ *                head * q_lat_stride_head + k], k < d; q_rope likewise, k < d_rope.  dtype
+ *                KVK_BF16, KVK_F16 or KVK_F32; strides in elements, multiples of 8
+ *   n_q          rows of the query and output tensors; n_q * n_heads < 2^31 (0: nothing launched)
+ *   dev_q_start  device int32 [batch + 1], ascending within [0, n_q]; otherwise KVK_FLAG_SEQ_LEN
+ *                and the call writes nothing
+ *   dev_seq_lens device int32 [batch], clamped to [0, table_pages * page_tokens] (and 2^30;
+ *                KVK_FLAG_SEQ_LEN)
+ *   dev_block_table  tokens on an entry outside the pool are skipped (KVK_FLAG_PAGE)
+ *   out          device, the queries' dtype, element (row, head, k < d) at out[row *
+ *                out_stride_tok + head * out_stride_head + k]; strides multiples of 8
+ *   lse          nullable device fp32 [n_q][n_heads] (natural log)
+ *   workspace    device, >= kvk_chunk_workspace_bytes(); contents are scratch.  Two calls that may
+ *                run at the same time need one each.
+ *
+ * A token whose cached row is not finite (KVK_FLAG_NONFINITE at its write) turns the rows that
+ * see it into NaN and no others.
+ * The CUDA-core kernel takes every call; kvk_set_decode_path applies.
+ */
+kvk_status kvk_mla_chunk(kvk_layout* layout, int layer, const void* q_lat, const void* q_rope,
+                         int dtype, int64_t q_lat_stride_tok, int64_t q_lat_stride_head,
+                         int64_t q_rope_stride_tok, int64_t q_rope_stride_head, int n_q, int batch,
+                         int n_heads, const int32_t* dev_q_start, const int32_t* dev_seq_lens,
+                         const int32_t* dev_block_table, int table_pages, int64_t table_stride,
+                         int page_tokens, float softmax_scale, void* out, int64_t out_stride_tok,
+                         int64_t out_stride_head, float* lse, void* workspace,
+                         size_t workspace_bytes, kvk_stream_t stream);
+
+/* Bytes of device workspace kvk_mla_chunk needs (it does not grow with n_q or batch today; pass
+ * the call's). */
+kvk_status kvk_chunk_workspace_bytes(const kvk_layout* layout, int layer, int n_q, int batch,
+                                     int n_heads, size_t* bytes);
+
+/* Which kernel kvk_mla_chunk takes for queries of this dtype (KVK_PATH_TENSOR or
+ * KVK_PATH_CUDA_CORE). */
+kvk_status kvk_chunk_path_for(const kvk_layout* layout, int layer, int dtype, int* path);
 
 /* Copy the sticky device flags to *flags (synchronises the stream); clear != 0 resets them
  * to zero afterwards. */

@@ -1,0 +1,78 @@
+"""Refusals of the paged entry points that need no GPU: every check that comes before a launch."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def kvk():
+    import __graft_entry__
+    __graft_entry__.build()
+    from compressed_decode_attention_kvk_b200 import kvk
+    return kvk
+
+
+@pytest.fixture()
+def lay(kvk):
+    """A planning-only layout: everything before its missing arena can be checked."""
+    handle, _, _ = kvk.kvk_create_layout([0, 0], [64, 0], [8, 0], 64, 16, 1, 256)
+    yield handle
+    kvk.kvk_destroy(handle)
+
+
+def P(x):
+    return ctypes.c_void_p(x)
+
+
+def test_layout_without_arena_is_refused(kvk, lay):
+    L = kvk._lib_handle()
+    p = P(4096)
+    assert L.kvk_paged_plan(lay, p, p, 1, p, p, 1, 16, p, 4, 4, 8, p, p, p, p, p, None) == 1
+    assert L.kvk_paged_write(lay, 0, p, 1, 64, p, 16, 1, p, None) == 1
+    assert L.kvk_mla_chunk(lay, 0, p, p, 1, 64, 64, 16, 16, 1, 1, 1, p, p, p, 4, 4, 16, 1.0, p, 64,
+                           64, None, p, 1 << 30, None) == 1
+    assert L.kvk_paged_plan(None, p, p, 1, p, p, 1, 16, p, 4, 4, 8, p, p, p, p, p, None) == 1
+
+
+def test_write_needs_an_anchor_layer(kvk, lay):
+    p = P(4096)
+    assert kvk._lib_handle().kvk_paged_write(lay, 1, p, 1, 64, p, 16, 1, p, None) == 4
+    assert kvk._lib_handle().kvk_paged_write(lay, 2, p, 1, 64, p, 16, 1, p, None) == 1
+
+
+def test_workspace_and_path_queries(kvk, lay):
+    assert kvk.kvk_chunk_workspace_bytes(lay, 0, 100, 4, 8) > 0
+    assert kvk.kvk_chunk_workspace_bytes(lay, 1, 0, 4096, 1) > 0
+    for bad in [(2, 1, 1, 1), (-1, 1, 1, 1), (0, -1, 1, 1), (0, 1, 0, 1), (0, 1, 4097, 1),
+                (0, 1, 1, 0), (0, 1, 1, 4097)]:
+        with pytest.raises(kvk.KvkError) as e:
+            kvk.kvk_chunk_workspace_bytes(lay, *bad)
+        assert e.value.status == 1
+    assert kvk.kvk_chunk_path_for(lay, 0, torch.float32) == kvk.KVK_PATH_CUDA_CORE
+    with pytest.raises(kvk.KvkError):
+        kvk.kvk_chunk_path_for(lay, 0, 9)
+    kvk.kvk_set_decode_path(lay, kvk.KVK_PATH_TENSOR)
+    with pytest.raises(kvk.KvkError) as e:
+        kvk.kvk_chunk_path_for(lay, 0, torch.float32)
+    assert e.value.status == 8
+
+
+def test_host_tensors_are_refused(kvk, lay):
+    t = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        kvk.kvk_paged_plan(lay, t, t, t, t, t.view(2, 2), 16, 4, t, t, t, t, t)
+    with pytest.raises(ValueError, match="CUDA"):
+        kvk.kvk_paged_write(lay, 0, torch.zeros(4, 64), torch.zeros(4, 16), t)
+    q = torch.zeros(4, 1, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        kvk.kvk_mla_chunk(lay, 0, q, q, t, t, t.view(2, 2), 16, 1.0, q, t)
+
+
+def test_row_stride_of_single_rows(kvk):
+    x = torch.zeros(3, 5, 64)
+    assert kvk._row_stride(x) == 320 and kvk._row_stride(x, 1) == 64
+    one = x[:1, :1]
+    assert kvk._row_stride(one) % 8 == 0 and kvk._row_stride(one) >= 64
+    assert kvk._row_stride(x[:, :, :0]) == 0
+    assert kvk._row_stride(x.expand(3, 5, 64)[:, :1]) == 320
