@@ -1,0 +1,1375 @@
+// kvk_chunk_tc.cu -- tensor-core (tcgen05) attention of chunks of new tokens over a paged cache.
+//
+// The rows of a sequence are its (new token, head) pairs, row = token * H + head: all of them
+// attend to the one latent stream, so 128 consecutive rows are one tile of
+//     S[128 rows x 128 tokens] = Q . C^T,   O[128 x d] += P . C[:, :d]
+// whatever the head count.  At d = 512 an O tile of 128 rows takes all of an SM's tensor memory,
+// so a tile belongs to a pair of CTAs (a cluster, tcgen05 cta_group::2, M = 128): each CTA holds
+// 64 rows of Q, S and O, supplies 64 of the 128 tokens to the score MMA and half the features to
+// the output MMA (N = 256 a step).  Measured rate of this form on B200, operands walking through
+// shared memory: 64 cycles per MMA at N = 256 (the full rate; one CTA alone reaches it only with
+// 128 rows, and takes 80 cycles for 64 rows with .ws), 46 at N = 128 (ideal 32).
+//
+// Work.  A row tile costs its 128-token blocks plus kPieceCost (query staging, output); every
+// cluster takes an equal slice of the batch's cost.  A tile that falls into several slices is
+// written as partials (running reference m, weight sum l, un-normalised o) and joined by
+// chunk_merge_kernel; a cluster owns at most two partial tiles, its first and its last, so the
+// workspace does not grow with the batch.
+//
+// Warps of a CTA (448 threads):
+//   0-3    softmax: a row and 64 tokens a thread; S from TMEM, P (16 bit) to shared memory, O
+//          rescaled when a row's reference grows by more than 2^8, outputs
+//   4-7    K team: own 64 tokens, packed codes -> 16-bit operand atoms (64 tokens x 64 features,
+//          128-byte swizzle) of a ring that the score MMA drains
+//   8-11   V team: all 128 tokens, this CTA's half of the latent features, for the output MMA
+//   12     MMA issuer (one thread of the leader CTA)
+//   13     token warp: walks the cluster's pieces, resolves pages to slots, loads token scales,
+//          warms L2 with the rows, four blocks ahead of the others
+// Both teams stage the query rows at a piece's start.
+//
+// Numbers.  Codes enter the MMA exactly: a code of at most 8 bits is an f16 integer; a 16-bit
+// code c and a group-scaled value c s are split into two f16 parts (hi = f16(x), lo = x - hi)
+// whose score MMAs add up.  The output MMA takes the high part (relative 2^-12) and P in f16
+// (2^-12); bf16 rows stay bf16, P too (2^-9, as the rows' own rounding).  A bf16 query is scaled
+// by a power of two of its row into f16's range (exact but for elements 2^-38 below the largest).
+// Scores, references and sums are fp32.
+//
+// Softmax with token scales.  With z_t the score in log2 units and s_t the token's scale, the
+// weight of code row t is s_t 2^(z_t): the kernel tracks w_t = z_t + log2 s_t, m >= max w_t - 8,
+// P_t = 2^(w_t - m) and l = sum P_t / s_t, so that P fits 16 bits whatever the scales.  A token
+// that does not exist (behind the end, or on a page outside the pool) has log2 s_t = -inf.
+#include <math_constants.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "kvk_chunk_tc.cuh"
+#include "kvk_decode_common.cuh"
+#include "kvk_sm100.cuh"
+
+namespace kvk {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 448;
+constexpr int kWarps = kThreads / 32;
+constexpr int kKWarp0 = 4, kVWarp0 = 8, kMmaWarp = 12, kTokWarp = 13;
+constexpr uint32_t kAtom = 8192;       // 64 rows x 128 bytes
+constexpr int kTokStages = 4;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSCol = 256;        // S buffers at 256 and 320 (64 columns); O at 0
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.0f;          // growth of a row's maximum that its reference lets pass
+constexpr int kSmemLimit = 232448;
+constexpr int kMaxK = 12;              // slots of the K ring
+constexpr uint64_t kDrainLimitNs = 2000000000ull;
+
+// One block of 128 tokens of a piece, published by the token warp.
+struct alignas(16) TokStage {
+  int32_t slot[128];
+  float sc[128], lsc[128], isc[128];   // s_t, log2 s_t, 1 / s_t
+  int32_t flags;                       // kEnd, kFirst, kLast
+  int32_t row0, flat0, rows;           // the sequence's first query row; the tile's first row
+                                       // within the sequence and the sequence's row count
+  int32_t len, count, t0;              // tokens, query tokens; first token of the block
+  int32_t piece;                       // running number of the piece
+  int32_t dest;                        // partial slot (0, 1) or -1: whole tile
+  int32_t seq, b1, nblk;               // for the partial's header
+};
+constexpr int kEnd = 1, kFirst = 2, kLast = 4;
+
+struct Shared {
+  TokStage tok[kTokStages];
+  int8_t qexp[4][64];                  // per row: e of its query's scaling 2^e
+  float xch[2][128];                   // row maxima of the two token halves
+  float xl[128];
+  uint64_t tok_full[kTokStages], tok_empty[kTokStages];
+  uint64_t k_full[kMaxK], k_empty[kMaxK];
+  uint64_t v_full[4], v_empty[4];
+  uint64_t q_full, q_empty, q_local[4];
+  uint64_t s_full[2], p_full, pv_done, x_bar, drain;
+  int64_t scan[kWarps + 1];
+  int64_t start_base;
+  int32_t start_seq, start_k;
+  uint32_t tmem_base, abort_word;
+};
+
+static_assert(sizeof(Shared) <= 11264, "leaves 27 atoms of 8 KB");
+
+// The fields of a piece's first block that query staging reads.
+struct QueryTile {
+  int row0, flat0, rows, piece;
+};
+
+struct TcChunk {
+  ChunkArgs a;
+  ChunkWork w;
+  int NL, NA, NV;          // latent atoms (padded to whole 128), all atoms, V atoms per CTA
+  int NK, NVS;             // K ring slots, V stages
+  uint32_t off_k, off_v, off_p, off_misc;
+  uint32_t idesc_s, idesc_o2, idesc_o1;   // score; output with 128 / 64 features per CTA
+  int q_bf16;
+};
+
+// ---- cluster-scope barriers -----------------------------------------------------------------
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                   map_rank(smem_u32(bar), rank))
+               : "memory");
+}
+__device__ __forceinline__ bool try_cl(uint64_t* b, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(b)), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// Arrives on the barrier of both CTAs once this thread's MMAs so far are complete.
+__device__ __forceinline__ void commit_both(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                     uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// 32 lanes x 32 columns: thread i of the warp holds lane base + i
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31, %32};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+      "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]),
+      "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]),
+      "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]),
+      "f"(v[29]), "f"(v[30]), "f"(v[31])
+      : "memory");
+}
+
+// Bounded waits of one call: a wait that runs out stops both CTAs.
+struct Waiter {
+  uint32_t abort_saddr;
+  uint64_t limit;
+  __device__ __forceinline__ bool operator()(uint64_t* b, uint32_t parity) const {
+    if (try_cl(b, parity, 0u)) return true;
+    const uint64_t t0 = globaltimer();
+    while (!try_cl(b, parity, 20000u)) {
+      if (abort_read(abort_saddr)) return false;
+      if (globaltimer() - t0 > limit) {
+#pragma unroll
+        for (uint32_t r = 0; r < 2; ++r)
+          asm volatile("st.volatile.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(abort_saddr, r)),
+                       "r"(1u)
+                       : "memory");
+        return false;
+      }
+    }
+    return true;
+  }
+};
+
+// ---- conversion of 16 consecutive elements --------------------------------------------------
+template <int BITS>
+constexpr int kRaw = BITS == 2 ? 1 : BITS == 4 ? 2 : BITS == 8 ? 4 : 8;   // 32-bit words
+template <int BITS, bool GROUP>
+constexpr bool kSplit = BITS == 16 || GROUP;   // two f16 parts in the score MMA
+template <int BITS>
+constexpr int kElemBits = BITS == KVK_BITS_BF16 ? 16 : BITS;
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
+  return __byte_perm(a, b, s);
+}
+__device__ __forceinline__ uint32_t h2add(uint32_t a, uint32_t b) {
+  const __half2 r = __hadd2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b),
+                            *reinterpret_cast<__half2*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t h2neg(uint32_t a) { return a ^ 0x80008000u; }
+constexpr uint32_t kH1024 = 0x64006400u;   // f16 1024: 0x6400 | u is the integer 1024 + u
+
+// four bytes, one field each, to f16 integers field - bias (bias as the f16 pair -(1024 + bias))
+__device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t bias, uint32_t* out) {
+  out[0] = h2add(prmt(w, kH1024, 0x7170), bias);
+  out[1] = h2add(prmt(w, kH1024, 0x7372), bias);
+}
+
+// The 16 elements of `raw` as two-element words: hi (the operand, or its high part) and, when
+// LO, the low part lo = x - hi.  s: the unit's group scale (f16 bits).
+template <int BITS, bool GROUP, bool LO>
+__device__ __forceinline__ void convert16(const uint32_t (&raw)[kRaw<BITS>], uint32_t s,
+                                          uint32_t (&hi)[8], uint32_t (&lo)[8]) {
+  if constexpr (BITS == KVK_BITS_BF16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) hi[i] = raw[i];
+  } else if constexpr (BITS == 16) {
+    // field u = 256 a + b, code c = 256 (a - 128) + b: A and b are exact f16 integers, one fused
+    // multiply-add rounds c to f16, and c - hi is exact (|256 A| >= b, or A = 0 and hi = b)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t A = h2add(prmt(raw[i], kH1024, 0x7371), 0xE480E480u);   // - 1152
+      const uint32_t B = h2add(prmt(raw[i], kH1024, 0x7270), 0xE400E400u);   // - 1024
+      const uint32_t h = h2fma(A, 0x5C005C00u, B);                           // 256 A + b
+      if constexpr (!GROUP) {
+        hi[i] = h;
+        if constexpr (LO) lo[i] = h2add(B, h2neg(h2fma(A, 0xDC00DC00u, h)));   // b - (h - 256 A)
+      } else {
+        // the product in fp32 (24 of its 27 bits), split into two f16 parts
+        const float sf = __half2float(__ushort_as_half((unsigned short)s));
+        const uint32_t r = raw[i] ^ 0x80008000u;
+        const float x0 = (float)(int)(short)(r & 0xFFFFu) * sf;
+        const float x1 = (float)(int)(short)(r >> 16) * sf;
+        const __half2 hh = __floats2half2_rn(x0, x1);
+        hi[i] = *reinterpret_cast<const uint32_t*>(&hh);
+        if constexpr (LO) {
+          const __half2 ll = __floats2half2_rn(x0 - __low2float(hh), x1 - __high2float(hh));
+          lo[i] = *reinterpret_cast<const uint32_t*>(&ll);
+        }
+      }
+    }
+  } else {
+    uint32_t c[8];
+    if constexpr (BITS == 8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bytes_to_f16(raw[i], 0xE480E480u, c + 2 * i);   // -(1024 + 128)
+    } else if constexpr (BITS == 4) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t x = raw[i] & 0x0F0F0F0Fu, y = (raw[i] >> 4) & 0x0F0F0F0Fu;
+        bytes_to_f16(prmt(x, y, 0x5140), 0xE408E408u, c + 4 * i);       // -(1024 + 8)
+        bytes_to_f16(prmt(x, y, 0x7362), 0xE408E408u, c + 4 * i + 2);
+      }
+    } else {
+      const uint32_t x0 = raw[0] & 0x03030303u, x1 = (raw[0] >> 2) & 0x03030303u,
+                     x2 = (raw[0] >> 4) & 0x03030303u, x3 = (raw[0] >> 6) & 0x03030303u;
+      const uint32_t p = prmt(x0, x1, 0x5140), q = prmt(x2, x3, 0x5140);
+      const uint32_t r = prmt(x0, x1, 0x7362), t = prmt(x2, x3, 0x7362);
+      bytes_to_f16(prmt(p, q, 0x5410), 0xE402E402u, c);                 // -(1024 + 2)
+      bytes_to_f16(prmt(p, q, 0x7632), 0xE402E402u, c + 2);
+      bytes_to_f16(prmt(r, t, 0x5410), 0xE402E402u, c + 4);
+      bytes_to_f16(prmt(r, t, 0x7632), 0xE402E402u, c + 6);
+    }
+    if constexpr (!GROUP) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hi[i] = c[i];
+    } else {
+      const uint32_t s2 = s | (s << 16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        hi[i] = h2mul(c[i], s2);
+        if constexpr (LO) lo[i] = h2fma(c[i], s2, h2neg(hi[i]));   // exact but for f16 subnormals
+      }
+    }
+  }
+}
+
+// Non-finite elements of a row.  A token whose row holds one must not reach the queries that do
+// not see it, although its zero weight multiplies it there: it goes into the score operand as
+// NaN (every query that sees it becomes NaN) and into the output operand as zero.
+template <bool BF16>
+__device__ __forceinline__ bool nonfinite16(const uint32_t (&w)[8]) {
+  const uint32_t e = BF16 ? 0x7F807F80u : 0x7C007C00u;
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t x = w[i] & e;   // a half equal to its exponent mask is inf or NaN
+    any |= ((x & 0xFFFFu) == (e & 0xFFFFu)) | ((x >> 16) == (e >> 16));
+  }
+  return any != 0;
+}
+template <bool BF16>
+__device__ __noinline__ void replace_nonfinite(uint32_t* w, uint32_t with) {
+  const uint32_t e = BF16 ? 0x7F80u : 0x7C00u;
+  for (int i = 0; i < 8; ++i) {
+    if ((w[i] & e) == e) w[i] = (w[i] & 0xFFFF0000u) | with;
+    if (((w[i] >> 16) & e) == e) w[i] = (w[i] & 0xFFFFu) | (with << 16);
+  }
+}
+
+template <int BITS, bool GROUP>
+struct Unit {
+  uint32_t w[kRaw<BITS>];
+  uint32_t s;
+};
+
+// 16 elements of row `slot` from element e (a multiple of 16) on; slot < 0: not read
+template <int BITS, bool GROUP>
+__device__ __forceinline__ void load_unit(const ChunkArgs& a, int slot, int e,
+                                          Unit<BITS, GROUP>& u) {
+  constexpr int RW = kRaw<BITS>;
+  if (slot < 0 || e < 0) return;
+  const uint8_t* p = a.codes + (int64_t)slot * a.row_bytes + e * kElemBits<BITS> / 8;
+  if constexpr (RW == 1) {
+    u.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  } else if constexpr (RW == 2) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    u.w[0] = v.x;
+    u.w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < RW / 4; ++i) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      u.w[4 * i] = v.x;
+      u.w[4 * i + 1] = v.y;
+      u.w[4 * i + 2] = v.z;
+      u.w[4 * i + 3] = v.w;
+    }
+  }
+  if constexpr (GROUP)
+    u.s = __ldg(reinterpret_cast<const unsigned short*>(a.scales) + (int64_t)slot * a.sg +
+                e / a.group);
+}
+
+// Store 16 converted elements of atom row t, columns 16 sub .. 16 sub + 15 (two 16-byte chunks
+// under the 128-byte swizzle)
+__device__ __forceinline__ void store_unit(uint32_t atom, int t, int sub, const uint32_t (&w)[8]) {
+  const uint32_t row = atom + (uint32_t)t * 128u;
+  sts128(row + (uint32_t)(((2 * sub) ^ (t & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+  sts128(row + (uint32_t)(((2 * sub + 1) ^ (t & 7)) << 4), make_uint4(w[4], w[5], w[6], w[7]));
+}
+
+// Element index of columns 16 sub.. of atom `at` (latent atoms, then RoPE atoms), -1: padding
+__device__ __forceinline__ int unit_elem(const TcChunk& P, int at, int sub) {
+  const int x = (at < P.NL ? at : at - P.NL) * 64 + 16 * sub;
+  if (at < P.NL) return x < P.a.d ? x : -1;
+  return x < P.a.d_rope ? P.a.d + x : -1;
+}
+
+__device__ __forceinline__ int blocks_of(int len, int count, int H, int flat0, int rows) {
+  // tokens that the tile's last row sees, in blocks of 128; one block where it sees none (its
+  // rows are written all the same)
+  const int last = min(flat0 + 128, rows) - 1;
+  const int64_t vis = (int64_t)len - count + last / H + 1;
+  const int v = (int)max((int64_t)0, min(vis, (int64_t)len));
+  return max(1, (v + 127) >> 7);
+}
+
+// Query rows [r0, r1) of this CTA's 64, by one warp: two rows at a time.  A bf16 query for f16
+// operands is scaled by the power of two that brings its row's largest element into
+// [2^14, 2^15); other queries are copied.  A negative softmax scale flips the sign.
+template <bool OP_BF16>
+__device__ __forceinline__ void stage_query(const TcChunk& P, Shared& S, uint32_t q_saddr,
+                                            const QueryTile& h, int rank, int r0, int r1) {
+  const int lane = threadIdx.x & 31;
+  const int chunks = P.NA * 8;                    // 16-byte chunks of 8 features
+  const bool scale = !OP_BF16 && P.q_bf16;
+  const uint32_t flip = P.a.sigma < 0.0f ? 0x80008000u : 0u;
+  constexpr int kC = 3;                           // chunks a lane: up to 96 (768 features)
+  constexpr int kR = 2;
+  const uint16_t* qlat = static_cast<const uint16_t*>(P.a.q_lat);
+  const uint16_t* qrope = static_cast<const uint16_t*>(P.a.q_rope);
+  for (int r = r0; r < r1; r += kR) {
+    uint4 v[kR][kC];
+#pragma unroll
+    for (int i = 0; i < kR; ++i) {
+      const int flat = h.flat0 + rank * 64 + r + i;
+      const bool ok = flat < h.rows;
+      const int j = ok ? flat / P.a.H : 0, hd = flat - j * P.a.H;
+      const uint16_t* pl = qlat + (int64_t)(h.row0 + j) * P.a.ql_st + (int64_t)hd * P.a.ql_sh;
+      const uint16_t* pr = qrope + (int64_t)(h.row0 + j) * P.a.qr_st + (int64_t)hd * P.a.qr_sh;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        const int ch = c * 32 + lane;
+        const int x = ch * 8 - (ch * 8 >= P.NL * 64 ? P.NL * 64 : 0);
+        v[i][c] = make_uint4(0u, 0u, 0u, 0u);
+        if (ok && ch < chunks) {
+          if (ch * 8 < P.NL * 64) {
+            if (x < P.a.d) v[i][c] = __ldg(reinterpret_cast<const uint4*>(pl + x));
+          } else if (x < P.a.d_rope) {
+            v[i][c] = __ldg(reinterpret_cast<const uint4*>(pr + x));
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kR; ++i) {
+      int e = 0;
+      float mul = 1.0f;
+      if (scale) {
+        uint32_t mx = 0;   // largest magnitude as bf16 bits (sign cleared: ordered as integers)
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+          const uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx = max(mx, max((w[k] & 0x7FFFu), ((w[k] >> 16) & 0x7FFFu)));
+        }
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        const int ex = (int)(mx >> 7);             // biased exponent of the largest
+        if (ex > 0 && ex < 255) {
+          // e = 14 - (ex - 127), kept where 2^e and 2^-e are normal numbers
+          e = max(-126, min(126, 141 - ex));
+          mul = __uint_as_float((uint32_t)(127 + e) << 23);
+        }
+      }
+      const int t = r + i;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        const int ch = c * 32 + lane;
+        if (ch >= chunks) continue;
+        uint32_t w[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (scale) {
+            const __half2 x = __floats2half2_rn(__uint_as_float(w[k] << 16) * mul,
+                                                __uint_as_float(w[k] & 0xFFFF0000u) * mul);
+            w[k] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          w[k] ^= flip;
+        }
+        sts128(q_saddr + (uint32_t)(ch >> 3) * kAtom + (uint32_t)t * 128u +
+                   (uint32_t)(((ch & 7) ^ (t & 7)) << 4),
+               make_uint4(w[0], w[1], w[2], w[3]));
+      }
+      if (lane == 0) S.qexp[h.piece & 3][t] = (int8_t)e;
+    }
+  }
+}
+
+// Exclusive prefix of v over the block; *total gets the sum.  All threads call it.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* buf, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) buf[warp] = x;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int64_t t = buf[w];
+    if (w < warp) before += t;
+    all += t;
+  }
+  *total = all;
+  return before + x - v;
+}
+
+template <int BITS, bool GROUP>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+chunk_tc_kernel(const __grid_constant__ TcChunk P) {
+  constexpr bool kBf16 = BITS == KVK_BITS_BF16;
+  constexpr bool kTok = !GROUP && !kBf16;             // one scale per token
+  constexpr bool kLo = kSplit<BITS, GROUP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const ChunkArgs& a = P.a;
+  Shared& S = *reinterpret_cast<Shared*>(smem + P.off_misc);
+  const uint32_t q_s = smem_u32(smem), k_s = q_s + P.off_k, v_s = q_s + P.off_v, p_s = q_s + P.off_p;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cta_rank();
+  const int cluster = blockIdx.x >> 1;
+  const int G = P.w.G;
+
+  if (tid == 0) {
+    S.abort_word = 0;
+    for (int i = 0; i < kTokStages; ++i) {
+      mbar_init(&S.tok_full[i], 1);
+      mbar_init(&S.tok_empty[i], 12 + (rank == 0 ? 1 : 0));
+    }
+    for (int i = 0; i < kMaxK; ++i) {
+      mbar_init(&S.k_full[i], 8);
+      mbar_init(&S.k_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&S.v_full[i], 8);
+      mbar_init(&S.v_empty[i], 1);
+      mbar_init(&S.q_local[i], 8);
+    }
+    mbar_init(&S.q_full, 16);
+    mbar_init(&S.q_empty, 1);
+    mbar_init(&S.s_full[0], 1);
+    mbar_init(&S.s_full[1], 1);
+    mbar_init(&S.p_full, 8);
+    mbar_init(&S.pv_done, 1);
+    mbar_init(&S.x_bar, 4);
+    mbar_init(&S.drain, 1);
+    fence_mbar_init();
+    // no partials of this cluster yet
+    if (rank == 0) {
+      P.w.head[cluster * 2].valid = 0;
+      P.w.head[cluster * 2 + 1].valid = 0;
+    }
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&S.tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+
+  // ---- this cluster's slice of the work -------------------------------------------------------
+  // tiles of every sequence (prefix sums in the ring's memory, not yet in use), then their costs
+  int32_t* pre = reinterpret_cast<int32_t*>(smem);
+  int64_t u0 = 0, u1 = 0;
+  {
+    const int per = (a.batch + kThreads - 1) / kThreads;
+    const int i0 = min(a.batch, tid * per), i1 = min(a.batch, i0 + per);
+    int64_t tiles = 0, total_tiles = 0, total = 0;
+    bool bad_rows = false, bad_len = false;
+    for (int i = i0; i < i1; ++i) {
+      const int s0 = __ldg(a.q_start + i), s1 = __ldg(a.q_start + i + 1), l = __ldg(a.seq_lens + i);
+      bad_rows = bad_rows || s0 < 0 || s1 < s0 || s1 > a.n_q;
+      bad_len = bad_len || l < 0 || l > a.cap;
+      tiles += ((int64_t)max(0, s1 - s0) * a.H + 127) >> 7;
+    }
+    const bool stop = __syncthreads_or(bad_rows) != 0;
+    if ((bad_rows || bad_len) && blockIdx.x == 0) atomicOr(a.flags, KVK_FLAG_SEQ_LEN);
+    int64_t at = block_scan(stop ? 0 : tiles, S.scan, &total_tiles);
+    if (!stop) {
+      for (int i = i0; i < i1; ++i) {
+        const int s0 = __ldg(a.q_start + i), s1 = __ldg(a.q_start + i + 1);
+        pre[i] = (int32_t)at;
+        at += ((int64_t)(s1 - s0) * a.H + 127) >> 7;
+      }
+      if (tid == 0) pre[a.batch] = (int32_t)total_tiles;
+    }
+    __syncthreads();
+    // costs of a run of consecutive tiles a thread
+    const int nt = (int)total_tiles;
+    const int tper = (nt + kThreads - 1) / kThreads;
+    const int f0 = min(nt, tid * tper), f1 = min(nt, f0 + tper);
+    int seq0 = 0;
+    if (f0 < f1) {
+      int lo = 0, hi = a.batch - 1;   // the last sequence whose tiles start at or before f0
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= f0) lo = mid; else hi = mid - 1;
+      }
+      seq0 = lo;
+    }
+    int64_t cost = 0, base = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+      int seq = seq0, loaded = -1;
+      ChunkSeq s = {0, 0, 0};
+      for (int f = f0; f < f1; ++f) {
+        while (pre[seq + 1] <= f) ++seq;
+        if (loaded != seq) {
+          bool b;
+          s = chunk_seq(a, seq, &b);
+          loaded = seq;
+        }
+        const int k = f - pre[seq];
+        const int c = kPieceCost + blocks_of(s.len, s.count, a.H, k * 128, s.count * a.H);
+        if (pass == 0) {
+          cost += c;
+        } else {
+          if (base <= u0 && u0 < base + c) {
+            S.start_seq = seq;
+            S.start_k = k;
+            S.start_base = base;
+          }
+          base += c;
+        }
+      }
+      if (pass == 0) {
+        base = block_scan(cost, S.scan, &total);
+        u0 = split_cost(cluster, total, G);
+        u1 = split_cost(cluster + 1, total, G);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers are initialised, both have allocated
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  const Waiter wait{smem_u32(&S.abort_word), a.limit_ns};
+  const int nch = (P.NV + 1) >> 1;       // output MMA steps over the features: 2 atoms, or the last 1
+
+  if (warp == kTokWarp) {
+    // ======================= token warp: pieces, slots, scales ==================================
+    int seq = S.start_seq, k = S.start_k;
+    int64_t base = S.start_base;
+    int g = 0, piece = 0;
+    bool ok = true;
+    if (u0 < u1) {
+      bool b;
+      ChunkSeq s = chunk_seq(a, seq, &b);
+      while (ok && base < u1) {
+        const int rows = s.count * a.H;
+        const int nblk = blocks_of(s.len, s.count, a.H, k * 128, rows);
+        const int64_t x0 = u0 - base - kPieceCost, x1 = u1 - base - kPieceCost;
+        const int b0 = (int)max((int64_t)0, min(x0, (int64_t)nblk));
+        const int b1 = (int)max((int64_t)0, min(x1, (int64_t)nblk));
+        for (int blk = b0; ok && blk < b1; ++blk, ++g) {
+          const int st = g % kTokStages;
+          ok = wait(&S.tok_empty[st], ((g / kTokStages) & 1) ^ 1);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          TokStage& T = S.tok[st];
+          const int t0 = blk << 7;
+          int sl[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = t0 + 32 * i + lane;
+            sl[i] = t < s.len ? chunk_slot(a, seq, t) : -1;
+          }
+          // the rows that this CTA converts for the scores are fetched into L2 now
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int my = rank ? sl[2 + i] : sl[i];
+            if (my >= 0)
+              asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                               a.codes + (int64_t)my * a.row_bytes),
+                           "r"(a.row_bytes)
+                           : "memory");
+          }
+          float sc[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sc[i] = (kTok && sl[i] >= 0) ? __half2float(a.scales[sl[i]]) : 1.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int x = 32 * i + lane;
+            T.slot[x] = sl[i];
+            if constexpr (kTok) {
+              // an all-zero token (scale 0) keeps its score 0; its weight multiplies zeros, so
+              // any positive scale serves
+              const float w = sc[i] == 0.0f ? 5.9604644775390625e-8f : sc[i];
+              T.sc[x] = sl[i] >= 0 ? sc[i] : 0.0f;
+              T.isc[x] = sl[i] >= 0 ? 1.0f / w : 0.0f;
+              T.lsc[x] = sl[i] >= 0 ? log2f(w) : -CUDART_INF_F;
+            } else {
+              T.lsc[x] = sl[i] >= 0 ? 0.0f : -CUDART_INF_F;
+            }
+          }
+          if (lane == 0) {
+            T.flags = (blk == b0 ? kFirst : 0) | (blk == b1 - 1 ? kLast : 0);
+            T.row0 = s.row0;
+            T.flat0 = k * 128;
+            T.rows = rows;
+            T.len = s.len;
+            T.count = s.count;
+            T.t0 = t0;
+            T.piece = piece;
+            T.dest = (b0 == 0 && b1 == nblk) ? -1 : (b0 > 0 ? 0 : 1);
+            T.seq = seq;
+            T.b1 = b1;
+            T.nblk = nblk;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.tok_full[st]);
+        }
+        if (b1 > b0) ++piece;
+        base += kPieceCost + nblk;
+        ++k;
+        if (base < u1 && k * 128 >= rows) {   // the next sequence that has query rows
+          k = 0;
+          ++seq;
+          while (seq < a.batch) {
+            const int i = seq + lane;
+            const bool has = i < a.batch && __ldg(a.q_start + i + 1) > __ldg(a.q_start + i);
+            const unsigned m = __ballot_sync(0xffffffffu, has);
+            if (m) {
+              seq += __ffs(m) - 1;
+              break;
+            }
+            seq += 32;
+          }
+          if (seq >= a.batch) break;
+          s = chunk_seq(a, seq, &b);
+        }
+      }
+    }
+    if (ok) {
+      const int st = g % kTokStages;
+      ok = __all_sync(0xffffffffu, wait(&S.tok_empty[st], ((g / kTokStages) & 1) ^ 1));
+      if (ok && lane == 0) {
+        S.tok[st].flags = kEnd;
+        mbar_arrive(&S.tok_full[st]);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ======================= MMA issuer =========================================================
+    if (rank == 0 && lane == 0) {
+      const uint64_t q0 = sdesc(q_s, 16u, 1024u, kLayoutSw128);
+      const uint64_t kb0 = sdesc(k_s, 16u, 1024u, kLayoutSw128);
+      const uint64_t p0 = sdesc(p_s, 16u, 1024u, kLayoutSw128);
+      const uint64_t vb0 = sdesc(v_s, kAtom, 1024u, kLayoutSw128);
+      int kslot = 0;
+      uint32_t kpar = 0;
+      bool first_prev = false;
+      // output MMAs of block g (its first of a piece starts the sums anew)
+      auto output = [&](int g, bool first) -> bool {
+        if (!wait(&S.p_full, g & 1)) return false;
+        tc_fence_after();
+        const int vs = g % P.NVS;
+        const uint32_t vpar = (g / P.NVS) & 1;
+        for (int ch = 0; ch < nch; ++ch) {
+          if (!wait(&S.v_full[vs * 2 + ch], vpar)) return false;
+          tc_fence_after();
+          const bool two = 2 * ch + 2 <= P.NV;
+          const uint32_t idesc = two ? P.idesc_o2 : P.idesc_o1;
+          const uint32_t hstep = (two ? 2 * kAtom : kAtom) >> 4;
+          const uint64_t vb = vb0 + ((uint32_t)(vs * 2 * P.NV + 4 * ch) * kAtom >> 4);
+          const uint32_t dcol = tmem + 128u * ch;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma2(dcol, p0 + (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2,
+                 vb + (kk >> 2) * hstep + (kk & 3) * 128, idesc, (kk > 0 || !first) ? 1u : 0u);
+          commit_both(&S.v_empty[vs * 2 + ch]);
+        }
+        commit_both(&S.pv_done);
+        return true;
+      };
+      bool ok = true;
+      int g = 0, pieces = 0;
+      for (;; ++g) {
+        const int st = g % kTokStages;
+        ok = wait(&S.tok_full[st], (g / kTokStages) & 1);
+        if (!ok) break;
+        const int fl = *const_cast<volatile int32_t*>(&S.tok[st].flags);
+        mbar_arrive(&S.tok_empty[st]);
+        if (fl & kEnd) break;
+        if (fl & kFirst) {
+          ok = wait(&S.q_full, pieces & 1);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t scol = tmem + kSCol + 64u * (g & 1);
+        const int parts = kLo ? 2 : 1;
+        for (int at = 0; ok && at < P.NA; ++at) {
+          for (int part = 0; part < parts; ++part) {
+            ok = wait(&S.k_full[kslot], kpar);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t ad = q0 + ((uint32_t)at * kAtom >> 4);
+            const uint64_t bd = kb0 + ((uint32_t)kslot * kAtom >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma2(scol, ad + kk * 2, bd + kk * 2, P.idesc_s,
+                   (at > 0 || part > 0 || kk > 0) ? 1u : 0u);
+            commit_both(&S.k_empty[kslot]);
+            if (++kslot == P.NK) {
+              kslot = 0;
+              kpar ^= 1;
+            }
+          }
+        }
+        if (!ok) break;
+        commit_both(&S.s_full[g & 1]);
+        if (fl & kLast) {
+          commit_both(&S.q_empty);
+          ++pieces;
+        }
+        if (g > 0) {
+          ok = output(g - 1, first_prev);
+          if (!ok) break;
+        }
+        first_prev = (fl & kFirst) != 0;
+      }
+      if (ok && g > 0) ok = output(g - 1, first_prev);
+      // every MMA and its arrivals are done before either CTA leaves
+      asm volatile(
+          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+              smem_u32(&S.drain))
+          : "memory");
+      const uint64_t t0 = globaltimer();
+      while (!try_cl(&S.drain, 0u, 20000u) && globaltimer() - t0 < kDrainLimitNs) {
+      }
+    }
+  } else if (warp >= kVWarp0) {
+    // ======================= V team =============================================================
+    const int vt = tid - kVWarp0 * 32, tq = vt >> 2, sub = vt & 3;
+    const int vw = warp - kVWarp0;
+    bool ok = true;
+    for (int g = 0;; ++g) {
+      const int st = g % kTokStages;
+      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], (g / kTokStages) & 1));
+      if (!ok) break;
+      const TokStage& T = S.tok[st];
+      const int fl = T.flags;
+      if (fl & kEnd) break;
+      int sl[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sl[u] = T.slot[tq + 32 * u];
+      Unit<BITS, GROUP> buf[2][4];
+      auto load = [&](int j, Unit<BITS, GROUP> (&b)[4]) {
+        const int e = unit_elem(P, (int)rank * P.NV + j, sub);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) load_unit<BITS, GROUP>(a, sl[u], e, b[u]);
+      };
+      load(0, buf[0]);
+      if (fl & kFirst) {
+        if (T.piece > 0) ok = wait(&S.q_empty, (T.piece - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const QueryTile head = {T.row0, T.flat0, T.rows, T.piece};
+        stage_query<kBf16>(P, S, q_s, head, (int)rank, 32 + vw * 8, 32 + vw * 8 + 8);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&S.q_local[T.piece & 3]);
+          arrive_at(&S.q_full, 0);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.tok_empty[st]);
+      const int vs = g % P.NVS;
+      const uint32_t vpar = ((g / P.NVS) & 1) ^ 1;
+      const uint32_t stage = v_s + (uint32_t)(vs * 2 * P.NV) * kAtom;
+      for (int j0 = 0; j0 < P.NV; j0 += 2) {
+        const int ch = j0 >> 1;
+        const bool two = j0 + 2 <= P.NV;
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+          const int j = j0 + jj;
+          if (j >= P.NV) break;
+          if (j + 1 < P.NV) load(j + 1, buf[(jj + 1) & 1]);
+          if (jj == 0) {
+            ok = __all_sync(0xffffffffu, wait(&S.v_empty[vs * 2 + ch], vpar));
+            if (!ok) break;
+          }
+          const int e = unit_elem(P, (int)rank * P.NV + j, sub);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t hi[8], lo[8];
+            if (sl[u] >= 0 && e >= 0) {
+              convert16<BITS, GROUP, false>(buf[jj & 1][u].w, buf[jj & 1][u].s, hi, lo);
+              if constexpr (kBf16 || GROUP) {
+                if (nonfinite16<kBf16>(hi)) replace_nonfinite<kBf16>(hi, 0u);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) hi[i] = 0u;
+            }
+            // [token half][atom of the step][64 tokens]
+            const uint32_t atom = stage + (uint32_t)(4 * ch + (u >> 1) * (two ? 2 : 1) + jj) * kAtom;
+            store_unit(atom, tq + 32 * (u & 1), sub, hi);
+          }
+        }
+        if (!ok) break;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_at(&S.v_full[vs * 2 + ch], 0);
+      }
+      if (!ok) break;
+    }
+  } else if (warp >= kKWarp0) {
+    // ======================= K team =============================================================
+    constexpr int D = 3;   // atoms whose loads are in flight
+    const int kt = tid - kKWarp0 * 32, tq = kt >> 2, sub = kt & 3;
+    const int kw = warp - kKWarp0;
+    int kslot = 0;
+    uint32_t kpar = 1;
+    bool ok = true;
+    int g = 0;             // next block to be taken from the token ring
+    for (;;) {             // one piece
+      int st = g % kTokStages;
+      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], (g / kTokStages) & 1));
+      if (!ok) break;
+      if (S.tok[st].flags & kEnd) break;
+      // prefetch cursor: atom pa of the block whose slots are in ps; more: further atoms exist
+      int ps[2], pa = 0;
+      bool more = true, last = false;
+      const int piece = S.tok[st].piece;
+      const QueryTile head = {S.tok[st].row0, S.tok[st].flat0, S.tok[st].rows, piece};
+      auto take = [&]() -> bool {   // the block of ring entry g into the cursor
+        const int s1 = g % kTokStages;
+        if (!__all_sync(0xffffffffu, wait(&S.tok_full[s1], (g / kTokStages) & 1))) return false;
+        const TokStage& T = S.tok[s1];
+        last = (T.flags & kLast) != 0;
+        ps[0] = T.slot[64 * (int)rank + tq];
+        ps[1] = T.slot[64 * (int)rank + tq + 32];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.tok_empty[s1]);
+        ++g;
+        return true;
+      };
+      ok = take();
+      if (!ok) break;
+      Unit<BITS, GROUP> buf[D][2];
+      int be[D];            // element index of the buffered unit (-1: padding), or -2: none
+      bool bz[D][2];        // its token exists
+      auto fetch = [&](int& e_out, bool (&z)[2], Unit<BITS, GROUP> (&b)[2]) -> bool {
+        if (pa == P.NA) {
+          if (last) more = false;
+          else {
+            if (!take()) return false;
+            pa = 0;
+          }
+        }
+        if (!more) {
+          e_out = -2;
+          return true;
+        }
+        const int e = unit_elem(P, pa, sub);
+        e_out = e;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          z[u] = ps[u] >= 0;
+          load_unit<BITS, GROUP>(a, ps[u], e, b[u]);
+        }
+        ++pa;
+        return true;
+      };
+#pragma unroll
+      for (int u = 0; u < D; ++u)
+        if (ok) ok = fetch(be[u], bz[u], buf[u]);
+      if (!ok) break;
+      if (piece > 0) ok = __all_sync(0xffffffffu, wait(&S.q_empty, (piece - 1) & 1));
+      if (!ok) break;
+      stage_query<kBf16>(P, S, q_s, head, (int)rank, kw * 8, kw * 8 + 8);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&S.q_local[piece & 3]);
+        arrive_at(&S.q_full, 0);
+      }
+      bool done = false;
+      while (!done) {
+#pragma unroll
+        for (int x = 0; x < D; ++x) {
+          // (the end is the same in every lane: it follows the ring's flags)
+          if (be[x] == -2) {
+            done = true;
+            break;
+          }
+          uint32_t hi[2][8], lo[2][8];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (bz[x][u] && be[x] >= 0) {
+              convert16<BITS, GROUP, kLo>(buf[x][u].w, buf[x][u].s, hi[u], lo[u]);
+              if constexpr (kBf16 || GROUP) {
+                if (nonfinite16<kBf16>(hi[u])) {
+                  replace_nonfinite<kBf16>(hi[u], 0x7FFFu);
+                  if constexpr (kLo) replace_nonfinite<kBf16>(lo[u], 0u);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) hi[u][i] = 0u, lo[u][i] = 0u;
+            }
+          }
+          ok = fetch(be[x], bz[x], buf[x]);
+          if (!ok) break;
+#pragma unroll
+          for (int part = 0; part < (kLo ? 2 : 1); ++part) {
+            ok = __all_sync(0xffffffffu, wait(&S.k_empty[kslot], kpar));
+            if (!ok) break;
+            const uint32_t atom = k_s + (uint32_t)kslot * kAtom;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) store_unit(atom, tq + 32 * u, sub, part ? lo[u] : hi[u]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_at(&S.k_full[kslot], 0);
+            if (++kslot == P.NK) {
+              kslot = 0;
+              kpar ^= 1;
+            }
+          }
+          if (!ok) break;
+        }
+        if (!ok) break;
+      }
+      if (!ok) break;
+    }
+  } else {
+    // ======================= softmax ============================================================
+    const int r = tid & 63, hh = tid >> 6;          // row of the CTA, token half
+    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+    const int oc = P.NV * 64;                        // O columns (features of one half)
+    float m = -CUDART_INF_F, l = 0.0f, rc = 0.0f;
+    int lim = 0, row_q = 0, row_h = 0;
+    bool row_ok = false;
+    bool ok = true;
+    uint32_t met = 0;
+    auto meet = [&]() -> bool {                      // the four warps, bounded like every wait
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.x_bar);
+      return __all_sync(0xffffffffu, wait(&S.x_bar, met++ & 1));
+    };
+    for (int g = 0;; ++g) {
+      const int st = g % kTokStages;
+      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], (g / kTokStages) & 1));
+      if (!ok) break;
+      const TokStage& T = S.tok[st];
+      const int fl = T.flags;
+      if (fl & kEnd) break;
+      if (fl & kFirst) {
+        const int piece = T.piece;
+        const int flat = T.flat0 + (int)rank * 64 + r;
+        row_ok = flat < T.rows;
+        const int j = row_ok ? flat / a.H : 0;
+        row_h = flat - j * a.H;
+        row_q = T.row0 + j;
+        lim = row_ok ? min(T.len, max(0, T.len - T.count + j + 1)) : 0;
+        ok = __all_sync(0xffffffffu, wait(&S.q_local[piece & 3], (piece >> 2) & 1));
+        if (!ok) break;
+        rc = fabsf(a.sigma) * kLog2e *
+             __uint_as_float((uint32_t)(127 - S.qexp[piece & 3][r]) << 23);   // 2^-e
+        m = -CUDART_INF_F;
+        l = 0.0f;
+      }
+      ok = __all_sync(0xffffffffu, wait(&S.s_full[g & 1], (g >> 1) & 1));
+      if (!ok) break;
+      tc_fence_after();
+      float s[64];
+      const uint32_t sb = tmem + kSCol + 64u * (g & 1) + lanes;
+      tmem_ld32(sb, s);
+      tmem_ld32(sb + 32, s + 32);
+      tmem_wait_ld();
+      // w_t = z_t + log2 s_t, and its maximum over this half
+      const float4* lsc4 = reinterpret_cast<const float4*>(T.lsc + 64 * hh);
+      const float4* sc4 = reinterpret_cast<const float4*>(T.sc + 64 * hh);
+      const int vis = lim - T.t0 - 64 * hh;          // columns that the row sees
+      float mx = -CUDART_INF_F;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float4 b = lsc4[i];
+        float4 c = make_float4(1.f, 1.f, 1.f, 1.f);
+        if constexpr (kTok) c = sc4[i];
+        const float bb[4] = {b.x, b.y, b.z, b.w}, cc[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float z = s[4 * i + k];
+          if constexpr (kTok) z *= cc[k];
+          s[4 * i + k] = fmaf(z, rc, bb[k]);
+        }
+      }
+      if (__any_sync(0xffffffffu, vis < 64)) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) s[i] = i < vis ? s[i] : -CUDART_INF_F;
+      }
+#pragma unroll
+      for (int i = 0; i < 64; ++i) mx = fmaxf(mx, s[i]);
+      S.xch[g & 1][tid] = mx;
+      ok = meet();
+      if (!ok) break;
+      mx = fmaxf(mx, S.xch[g & 1][tid ^ 64]);
+      float alpha = 1.0f;
+      if (mx > m + kLazy) {
+        alpha = exp2f(m - mx);   // m = -inf: 0
+        l *= alpha;
+        m = mx;
+      }
+      const float mref = m == -CUDART_INF_F ? 0.0f : m;
+      uint32_t pk[32];
+      const float4* isc4 = reinterpret_cast<const float4*>(T.isc + 64 * hh);
+      float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float4 c = make_float4(1.f, 1.f, 1.f, 1.f);
+        if constexpr (kTok) c = isc4[i];
+        const float cc[4] = {c.x, c.y, c.z, c.w};
+        float e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          e[k] = ex2_approx(s[4 * i + k] - mref);
+          if (k & 1) l1 = fmaf(e[k], cc[k], l1); else l0 = fmaf(e[k], cc[k], l0);
+        }
+        if constexpr (kBf16) {
+          const __nv_bfloat162 x = __floats2bfloat162_rn(e[0], e[1]);
+          const __nv_bfloat162 y = __floats2bfloat162_rn(e[2], e[3]);
+          pk[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
+          pk[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
+        } else {
+          const __half2 x = __floats2half2_rn(e[0], e[1]);
+          const __half2 y = __floats2half2_rn(e[2], e[3]);
+          pk[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
+          pk[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+      }
+      l += l0 + l1;
+      // the scales and this block's header have been read
+      const int last = fl & kLast, dest = T.dest, t_seq = T.seq, t_b1 = T.b1, t_nblk = T.nblk;
+      const int t_flat0 = T.flat0, t_row0 = T.row0, t_rows = T.rows;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.tok_empty[st]);
+      // the previous output MMA has read P and left O
+      if (g > 0) {
+        ok = __all_sync(0xffffffffu, wait(&S.pv_done, (g - 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (!(fl & kFirst) && __any_sync(0xffffffffu, alpha != 1.0f)) {
+        for (int c = 0; c < oc; c += 32) {
+          float o[32];
+          tmem_ld32(tmem + c + lanes, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= alpha;
+          tmem_st32(tmem + c + lanes, o);
+        }
+        tmem_wait_st();
+      }
+      {
+        const uint32_t row = p_s + (uint32_t)hh * kAtom + (uint32_t)r * 128u;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          sts128(row + (uint32_t)((c ^ (r & 7)) << 4),
+                 make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]));
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_at(&S.p_full, 0);
+      if (!last) continue;
+
+      // ---- the piece's output ----
+      S.xl[tid] = l;
+      ok = meet();
+      if (!ok) break;
+      const float lt = l + S.xl[tid ^ 64];
+      ok = __all_sync(0xffffffffu, wait(&S.pv_done, g & 1));
+      if (!ok) break;
+      tc_fence_after();
+      const int f0 = hh * oc;                        // first feature of this thread
+      const int part = (cluster * 2 + dest) * 128 + (int)rank * 64 + r;
+      // a sum of zero: no token seen (or none that exists)
+      const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
+      uint16_t* orow = static_cast<uint16_t*>(a.out) + (int64_t)row_q * a.o_st +
+                       (int64_t)row_h * a.o_sh;
+      for (int c = 0; c < oc; c += 32) {
+        float o[32];
+        tmem_ld32(tmem + c + lanes, o);
+        tmem_wait_ld();
+        if (!row_ok) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {                // d is a multiple of 16
+          const int f = f0 + c + 8 * q;
+          if (f >= a.d) break;
+          if (dest >= 0) {
+            float* po = P.w.o + (int64_t)part * a.d + f;
+            *reinterpret_cast<float4*>(po) =
+                make_float4(o[8 * q], o[8 * q + 1], o[8 * q + 2], o[8 * q + 3]);
+            *reinterpret_cast<float4*>(po + 4) =
+                make_float4(o[8 * q + 4], o[8 * q + 5], o[8 * q + 6], o[8 * q + 7]);
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack_out(P.q_bf16, o[8 * q + 2 * k] * inv, o[8 * q + 2 * k + 1] * inv);
+            *reinterpret_cast<uint4*>(orow + f) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (hh == 0 && row_ok) {
+        if (dest >= 0) {
+          P.w.ml[2 * (int64_t)part] = m;
+          P.w.ml[2 * (int64_t)part + 1] = lt;
+        } else if (a.lse) {
+          a.lse[(int64_t)row_q * a.H + row_h] =
+              lt == 0.0f ? -CUDART_INF_F : kLn2 * (m + log2f(lt));
+        }
+      }
+      if (dest >= 0 && rank == 0 && tid == 0) {
+        ChunkPartial& h = P.w.head[cluster * 2 + dest];
+        h.seq = t_seq;
+        h.flat0 = t_flat0;
+        h.row0 = t_row0;
+        h.rows = t_rows;
+        h.b1 = t_b1;
+        h.nblk = t_nblk;
+        h.valid = 1;
+      }
+      tc_fence_before();
+    }
+  }
+  // a wait that ran out anywhere stops both CTAs; each reports it
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && abort_read(smem_u32(&S.abort_word))) atomicOr(a.flags, KVK_FLAG_TIMEOUT);
+  cluster_sync();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+}
+
+// ---------------------------------------------------------------------------------------
+// join of the row tiles that several clusters worked on
+// ---------------------------------------------------------------------------------------
+constexpr int kMergeWarps = 8;
+
+// CTA (g, y): if the last piece of cluster g began a tile it did not finish, rows y, y +
+// gridDim.y, ... (one a warp) of that tile, whose further pieces are the first ones of clusters
+// g + 1, ... up to the one that ends it.
+__global__ void __launch_bounds__(kMergeWarps * 32)
+chunk_merge_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ ChunkWork w,
+                   int q_bf16) {
+  const int g = blockIdx.x, lane = threadIdx.x & 31;
+  const ChunkPartial h = w.head[2 * g + 1];
+  if (!h.valid) return;
+  const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int flat = h.flat0 + row;
+  if (flat >= h.rows) return;
+  int end = g + 1;                       // pieces: (g, 1), (g + 1, 0), ..., (end - 1, 0)
+  for (bool done = false; !done && end < w.G; ++end) {
+    const ChunkPartial& x = w.head[2 * end];
+    if (x.valid && (x.seq != h.seq || x.flat0 != h.flat0)) break;
+    done = x.valid && x.b1 == x.nblk;
+  }
+  auto slot = [&](int c) { return (int64_t)(2 * c + (c == g ? 1 : 0)) * 128 + row; };
+  auto live = [&](int c) { return c == g || w.head[2 * c].valid; };
+  float M = -CUDART_INF_F;
+  for (int c = g; c < end; ++c)
+    if (live(c)) M = fmaxf(M, w.ml[2 * slot(c)]);
+  const int j = flat / a.H, hd = flat - j * a.H;
+  uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(h.row0 + j) * a.o_st +
+                  (int64_t)hd * a.o_sh;
+  const float ref = M == -CUDART_INF_F ? 0.0f : M;
+  float l = 0.0f;
+  for (int c = g; c < end; ++c)
+    if (live(c)) l += exp2f(w.ml[2 * slot(c)] - ref) * w.ml[2 * slot(c) + 1];
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  for (int f = 4 * lane; f < a.d; f += 128) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = g; c < end; ++c) {
+      if (!live(c)) continue;
+      const float x = exp2f(w.ml[2 * slot(c)] - ref);
+      const float4 o = *reinterpret_cast<const float4*>(w.o + slot(c) * a.d + f);
+      acc.x = fmaf(x, o.x, acc.x);
+      acc.y = fmaf(x, o.y, acc.y);
+      acc.z = fmaf(x, o.z, acc.z);
+      acc.w = fmaf(x, o.w, acc.w);
+    }
+    *reinterpret_cast<uint2*>(out + f) = make_uint2(pack_out(q_bf16, acc.x * inv, acc.y * inv),
+                                                    pack_out(q_bf16, acc.z * inv, acc.w * inv));
+  }
+  if (a.lse && lane == 0)
+    a.lse[(int64_t)(h.row0 + j) * a.H + hd] = l == 0.0f ? -CUDART_INF_F : kLn2 * (M + log2f(l));
+}
+
+__host__ constexpr uint32_t idesc_of(bool bf16, int N, bool b_mn) {
+  return idesc_f16(128, N, false, b_mn) | (bf16 ? (1u << 7) | (1u << 10) : 0u);
+}
+
+template <int BITS, bool GROUP>
+cudaError_t launch(const TcChunk& P, size_t smem, cudaStream_t st) {
+  auto k = chunk_tc_kernel<BITS, GROUP>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  k<<<dim3(2 * P.w.G), dim3(kThreads), smem, st>>>(P);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool chunk_tc_supported(const kvk_layout* L, const AnchorDesc& A, int dtype) {
+  if (dtype != KVK_BF16 && dtype != KVK_F16) return false;
+  // bf16 rows stay bf16 in the MMA, whose two operands have one type
+  if (A.b == KVK_BITS_BF16 && dtype != KVK_BF16) return false;
+  return A.d <= 512 && L->d_rope <= 64 && L->d_rope % 16 == 0;
+}
+
+cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkWork& w, int dtype, cudaStream_t st) {
+  TcChunk P;
+  memset(&P, 0, sizeof(P));
+  P.a = a;
+  P.w = w;
+  P.NL = (a.d + 127) / 128 * 2;
+  P.NA = P.NL + (a.d_rope + 63) / 64;
+  P.NV = P.NL / 2;
+  P.NVS = P.NV <= 2 ? 2 : 1;
+  const int room = (int)((kSmemLimit - (int)sizeof(Shared)) / (int)kAtom) - P.NA - 2 * P.NV * P.NVS - 2;
+  P.NK = std::min(kMaxK, room);
+  P.off_k = (uint32_t)P.NA * kAtom;
+  P.off_v = P.off_k + (uint32_t)P.NK * kAtom;
+  P.off_p = P.off_v + (uint32_t)(2 * P.NV * P.NVS) * kAtom;
+  P.off_misc = P.off_p + 2 * kAtom;
+  const bool bf = a.b == KVK_BITS_BF16;
+  P.idesc_s = idesc_of(bf, 128, false);
+  P.idesc_o2 = idesc_of(bf, 256, true);
+  P.idesc_o1 = idesc_of(bf, 128, true);
+  P.q_bf16 = dtype == KVK_BF16;
+  const size_t smem = P.off_misc + sizeof(Shared);
+  // the prologue's prefix sums use the rings' memory
+  if (P.NK < 2 || smem > (size_t)kSmemLimit || (size_t)(a.batch + 1) * 4 > P.off_misc)
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaErrorInvalidValue;
+  if (a.group) {
+    if (a.b == 2) e = launch<2, true>(P, smem, st);
+    else if (a.b == 4) e = launch<4, true>(P, smem, st);
+    else if (a.b == 8) e = launch<8, true>(P, smem, st);
+    else if (a.b == 16) e = launch<16, true>(P, smem, st);
+  } else {
+    if (a.b == KVK_BITS_BF16) e = launch<KVK_BITS_BF16, false>(P, smem, st);
+    else if (a.b == 2) e = launch<2, false>(P, smem, st);
+    else if (a.b == 4) e = launch<4, false>(P, smem, st);
+    else if (a.b == 8) e = launch<8, false>(P, smem, st);
+    else if (a.b == 16) e = launch<16, false>(P, smem, st);
+  }
+  if (e != cudaSuccess) return e;
+  chunk_merge_kernel<<<dim3(w.G, 128 / kMergeWarps), dim3(kMergeWarps * 32), 0, st>>>(a, w, P.q_bf16);
+  return cudaGetLastError();
+}
+
+size_t chunk_workspace(int d, int G, void* base, ChunkWork* w) {
+  size_t off = 0;
+  const size_t o_head = off;
+  off = align_up_sz(off + sizeof(ChunkPartial) * 2 * (size_t)G, 256);
+  const size_t o_ml = off;
+  off = align_up_sz(off + sizeof(float) * 2 * 128 * 2 * (size_t)G, 256);
+  const size_t o_o = off;
+  off = align_up_sz(off + sizeof(float) * (size_t)d * 128 * 2 * (size_t)G, 256);
+  if (base && w) {
+    uint8_t* p = static_cast<uint8_t*>(base);
+    w->head = reinterpret_cast<ChunkPartial*>(p + o_head);
+    w->ml = reinterpret_cast<float*>(p + o_ml);
+    w->o = reinterpret_cast<float*>(p + o_o);
+    w->G = G;
+  }
+  return off;
+}
+
+}  // namespace kvk

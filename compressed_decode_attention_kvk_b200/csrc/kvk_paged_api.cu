@@ -4,7 +4,7 @@
 
 #include <algorithm>
 
-#include "kvk_paged.cuh"
+#include "kvk_chunk_tc.cuh"
 
 using kvk::AnchorDesc;
 
@@ -32,9 +32,14 @@ int page_shift(int page_tokens) {
 
 int64_t pool_slots(const kvk_layout* L) { return (int64_t)L->max_batch * L->max_tokens; }
 
-// The kernel a chunk call takes, or -1.
+int chunk_clusters(const kvk_layout* L) {
+  return std::max(1, (L->num_sms > 0 ? L->num_sms : 148) / 2);
+}
+
+// The kernel a chunk call takes, or -1: the tensor-core kernel where it applies (bf16 and f16
+// queries), the CUDA-core kernel otherwise, as the layout's decode path allows.
 int chunk_path(const kvk_layout* L, const AnchorDesc& A, int dtype) {
-  (void)dtype;
+  if (L->path != KVK_PATH_CUDA_CORE && kvk::chunk_tc_supported(L, A, dtype)) return KVK_PATH_TENSOR;
   if (L->path == KVK_PATH_TENSOR || L->path == KVK_PATH_TENSOR_GENERAL) return -1;
   return kvk::chunk_fma_fits(A.n) ? KVK_PATH_CUDA_CORE : -1;
 }
@@ -133,7 +138,7 @@ kvk_status kvk_chunk_workspace_bytes(const kvk_layout* L, int layer, int n_q, in
   if (!L || !bytes || layer < 0 || layer >= L->n_layers || n_q < 0 || batch < 1 ||
       batch > kvk::kMaxPagedBatch || n_heads < 1 || n_heads > 4096)
     return KVK_ERR_INVALID_ARG;
-  *bytes = 256;   // the CUDA-core kernel needs none
+  *bytes = kvk::chunk_workspace(L->anchors[L->slot[layer]].d, chunk_clusters(L), nullptr, nullptr);
   return KVK_OK;
 }
 
@@ -207,7 +212,16 @@ kvk_status kvk_mla_chunk(kvk_layout* L, int layer, const void* q_lat, const void
   a.flags = reinterpret_cast<uint32_t*>(L->arena);
   a.limit_ns = L->wait_limit_ns ? L->wait_limit_ns : kvk::kDefaultWaitLimitNs;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = kvk::launch_chunk_fma(a, dtype, st);
+  cudaError_t e;
+  if (path == KVK_PATH_TENSOR) {
+    kvk::ChunkWork w;
+    memset(&w, 0, sizeof(w));
+    if (workspace_bytes < kvk::chunk_workspace(A.d, chunk_clusters(L), workspace, &w))
+      return KVK_ERR_WORKSPACE;
+    e = kvk::launch_chunk_tc(a, w, dtype, st);
+  } else {
+    e = kvk::launch_chunk_fma(a, dtype, st);
+  }
   return e == cudaSuccess ? KVK_OK : KVK_ERR_CUDA;
 }
 

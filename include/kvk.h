@@ -465,8 +465,10 @@ kvk_status kvk_paged_write(kvk_layout* layout, int layer, const void* c_kv, int 
  *                run at the same time need one each.
  *
  * A token whose cached row is not finite (KVK_FLAG_NONFINITE at its write) turns the rows that
- * see it into NaN and no others.
- * The CUDA-core kernel takes every call; kvk_set_decode_path applies.
+ * see it into NaN and no others.  Group-scaled values and f16 queries are held to the f16 range
+ * by the tensor-core kernel.  That kernel takes bf16 queries (and f16 ones, except over
+ * uncompressed anchors) with d <= 512, d_rope <= 64 and d_rope % 16 == 0; other calls take the
+ * CUDA-core kernel.  kvk_set_decode_path and kvk_set_wait_limit apply.
  */
 kvk_status kvk_mla_chunk(kvk_layout* layout, int layer, const void* q_lat, const void* q_rope,
                          int dtype, int64_t q_lat_stride_tok, int64_t q_lat_stride_head,

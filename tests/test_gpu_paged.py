@@ -300,7 +300,7 @@ CHUNKS = {   # lens, q_lens, heads, page
 
 @pytest.mark.parametrize("case", CHUNKS, ids=str)
 @pytest.mark.parametrize("b,G", FORMATS)
-@pytest.mark.parametrize("path", ["cuda_core"])
+@pytest.mark.parametrize("path", ["cuda_core", "tensor"])
 def test_chunk_matches_reference(pkg, oracle_mod, path, case, b, G):
     lens, q_lens, H, page = CHUNKS[case]
     pool = Pool(pkg, oracle_mod, lens, 128, 64, b, G, page, 11 + b)
@@ -335,3 +335,14 @@ def test_chunk_shapes_and_types(pkg, oracle_mod, d, dR, dtype, b):
         assert pool.lay.read_status() == 0
     finally:
         pool.lay.close()
+
+
+def test_chunk_takes_the_tensor_kernel(pkg):
+    for b, dtype, want in [(16, torch.bfloat16, 1), (8, torch.float16, 1), (4, torch.float32, 2),
+                           (0, torch.bfloat16, 1), (0, torch.float16, 2)]:
+        lay = pkg.Layout([0], [512], [b], 512, 64, 1, 64)
+        assert lay.chunk_path_for(0, dtype) == want
+        lay.close()
+    lay = pkg.Layout([0], [528], [8], 528, 64, 1, 64)
+    assert lay.chunk_path_for(0, torch.bfloat16) == pkg.KVK_PATH_CUDA_CORE
+    lay.close()
