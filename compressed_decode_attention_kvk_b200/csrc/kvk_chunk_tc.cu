@@ -16,7 +16,7 @@
 // chunk_merge_kernel; a cluster owns at most two partial tiles, its first and its last, so the
 // workspace does not grow with the batch.
 //
-// Warps of a CTA (448 threads):
+// Warps of a CTA (480 threads):
 //   0-3    softmax: a row and 64 tokens a thread; S from TMEM, P (16 bit) to shared memory, O
 //          rescaled when a row's reference grows by more than 2^8, outputs
 //   4-7    K team: own 64 tokens, packed codes -> 16-bit operand atoms (64 tokens x 64 features,
@@ -25,6 +25,7 @@
 //   12     MMA issuer (one thread of the leader CTA)
 //   13     token warp: walks the cluster's pieces, resolves pages to slots, loads token scales,
 //          warms L2 with the rows, four blocks ahead of the others
+//   14     relay: passes the barriers of written operands on to the leader
 // Both teams stage the query rows at a piece's start.
 //
 // Numbers.  Codes enter the MMA exactly: a code of at most 8 bits is an f16 integer; a 16-bit
@@ -43,6 +44,7 @@
 
 #include <algorithm>
 
+#include "kvk_chunk_convert.cuh"
 #include "kvk_chunk_tc.cuh"
 #include "kvk_decode_common.cuh"
 #include "kvk_sm100.cuh"
@@ -51,10 +53,11 @@ namespace kvk {
 namespace {
 
 using namespace sm100;
+using namespace chunk;
 
-constexpr int kThreads = 448;
+constexpr int kThreads = 480;
 constexpr int kWarps = kThreads / 32;
-constexpr int kKWarp0 = 4, kVWarp0 = 8, kMmaWarp = 12, kTokWarp = 13;
+constexpr int kKWarp0 = 4, kVWarp0 = 8, kMmaWarp = 12, kTokWarp = 13, kRelayWarp = 14;
 constexpr uint32_t kAtom = 8192;       // 64 rows x 128 bytes
 constexpr int kTokStages = 4;
 constexpr uint32_t kTmemCols = 512;
@@ -86,10 +89,11 @@ struct Shared {
   float xch[2][128];                   // row maxima of the two token halves
   float xl[128];
   uint64_t tok_full[kTokStages], tok_empty[kTokStages];
-  uint64_t k_full[kMaxK], k_empty[kMaxK];
-  uint64_t v_full[4], v_empty[4];
-  uint64_t q_full, q_empty, q_local[4];
-  uint64_t s_full[2], p_full, pv_done, x_bar, drain;
+  // operands: written (by this CTA's warps), passed on (to the leader, by both relays), free
+  uint64_t k_full[kMaxK], k_ready[kMaxK], k_empty[kMaxK];
+  uint64_t v_land[4], v_full[4], v_ready[4], v_empty[4];
+  uint64_t q_full, q_ready, q_empty, q_local[4];
+  uint64_t s_full[2], p_full, p_ready, pv_done, x_bar, drain;
   int64_t scan[kWarps + 1];
   int64_t start_base;
   int32_t start_seq, start_k;
@@ -111,7 +115,18 @@ struct TcChunk {
   uint32_t off_k, off_v, off_p, off_misc;
   uint32_t idesc_s, idesc_o2, idesc_o1;   // score; output with 128 / 64 features per CTA
   int q_bf16;
+  // expanded rows (kExp)
+  const float* mark;       // per slot: 0, or NaN for a row with non-finite elements
+  int box;                 // rows of a tensor-map box: min(page tokens, 64)
+  int pool_slots;
 };
+
+// A stopped kernel's copies: waits for a phase that its loads complete.
+__device__ __forceinline__ void drain(uint64_t* b, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_hint(b, parity, 20000u) && globaltimer() - t0 < kDrainLimitNs) {
+  }
+}
 
 // ---- cluster-scope barriers -----------------------------------------------------------------
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -124,21 +139,13 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
+// Arrives on the barrier of the pair's CTA `rank`.  What it orders is this CTA's shared memory, read
+// by this SM's tensor core, so CTA scope serves; at cluster scope the arrival waits for this
+// SM's global accesses too (measured about 1000 cycles).
 __device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(
                    map_rank(smem_u32(bar), rank))
                : "memory");
-}
-__device__ __forceinline__ bool try_cl(uint64_t* b, uint32_t parity, uint32_t ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(b)), "r"(parity), "r"(ns)
-      : "memory");
-  return ok != 0;
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
@@ -195,9 +202,9 @@ struct Waiter {
   uint32_t abort_saddr;
   uint64_t limit;
   __device__ __forceinline__ bool operator()(uint64_t* b, uint32_t parity) const {
-    if (try_cl(b, parity, 0u)) return true;
+    if (mbar_try(b, parity)) return true;
     const uint64_t t0 = globaltimer();
-    while (!try_cl(b, parity, 20000u)) {
+    while (!mbar_try_hint(b, parity, 20000u)) {
       if (abort_read(abort_saddr)) return false;
       if (globaltimer() - t0 > limit) {
 #pragma unroll
@@ -211,165 +218,6 @@ struct Waiter {
     return true;
   }
 };
-
-// ---- conversion of 16 consecutive elements --------------------------------------------------
-template <int BITS>
-constexpr int kRaw = BITS == 2 ? 1 : BITS == 4 ? 2 : BITS == 8 ? 4 : 8;   // 32-bit words
-template <int BITS, bool GROUP>
-constexpr bool kSplit = BITS == 16 || GROUP;   // two f16 parts in the score MMA
-template <int BITS>
-constexpr int kElemBits = BITS == KVK_BITS_BF16 ? 16 : BITS;
-
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
-  return __byte_perm(a, b, s);
-}
-__device__ __forceinline__ uint32_t h2add(uint32_t a, uint32_t b) {
-  const __half2 r = __hadd2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c) {
-  const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b),
-                            *reinterpret_cast<__half2*>(&c));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t h2neg(uint32_t a) { return a ^ 0x80008000u; }
-constexpr uint32_t kH1024 = 0x64006400u;   // f16 1024: 0x6400 | u is the integer 1024 + u
-
-// four bytes, one field each, to f16 integers field - bias (bias as the f16 pair -(1024 + bias))
-__device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t bias, uint32_t* out) {
-  out[0] = h2add(prmt(w, kH1024, 0x7170), bias);
-  out[1] = h2add(prmt(w, kH1024, 0x7372), bias);
-}
-
-// The 16 elements of `raw` as two-element words: hi (the operand, or its high part) and, when
-// LO, the low part lo = x - hi.  s: the unit's group scale (f16 bits).
-template <int BITS, bool GROUP, bool LO>
-__device__ __forceinline__ void convert16(const uint32_t (&raw)[kRaw<BITS>], uint32_t s,
-                                          uint32_t (&hi)[8], uint32_t (&lo)[8]) {
-  if constexpr (BITS == KVK_BITS_BF16) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) hi[i] = raw[i];
-  } else if constexpr (BITS == 16) {
-    // field u = 256 a + b, code c = 256 (a - 128) + b: A and b are exact f16 integers, one fused
-    // multiply-add rounds c to f16, and c - hi is exact (|256 A| >= b, or A = 0 and hi = b)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t A = h2add(prmt(raw[i], kH1024, 0x7371), 0xE480E480u);   // - 1152
-      const uint32_t B = h2add(prmt(raw[i], kH1024, 0x7270), 0xE400E400u);   // - 1024
-      const uint32_t h = h2fma(A, 0x5C005C00u, B);                           // 256 A + b
-      if constexpr (!GROUP) {
-        hi[i] = h;
-        if constexpr (LO) lo[i] = h2add(B, h2neg(h2fma(A, 0xDC00DC00u, h)));   // b - (h - 256 A)
-      } else {
-        // the product in fp32 (24 of its 27 bits), split into two f16 parts
-        const float sf = __half2float(__ushort_as_half((unsigned short)s));
-        const uint32_t r = raw[i] ^ 0x80008000u;
-        const float x0 = (float)(int)(short)(r & 0xFFFFu) * sf;
-        const float x1 = (float)(int)(short)(r >> 16) * sf;
-        const __half2 hh = __floats2half2_rn(x0, x1);
-        hi[i] = *reinterpret_cast<const uint32_t*>(&hh);
-        if constexpr (LO) {
-          const __half2 ll = __floats2half2_rn(x0 - __low2float(hh), x1 - __high2float(hh));
-          lo[i] = *reinterpret_cast<const uint32_t*>(&ll);
-        }
-      }
-    }
-  } else {
-    uint32_t c[8];
-    if constexpr (BITS == 8) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) bytes_to_f16(raw[i], 0xE480E480u, c + 2 * i);   // -(1024 + 128)
-    } else if constexpr (BITS == 4) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t x = raw[i] & 0x0F0F0F0Fu, y = (raw[i] >> 4) & 0x0F0F0F0Fu;
-        bytes_to_f16(prmt(x, y, 0x5140), 0xE408E408u, c + 4 * i);       // -(1024 + 8)
-        bytes_to_f16(prmt(x, y, 0x7362), 0xE408E408u, c + 4 * i + 2);
-      }
-    } else {
-      const uint32_t x0 = raw[0] & 0x03030303u, x1 = (raw[0] >> 2) & 0x03030303u,
-                     x2 = (raw[0] >> 4) & 0x03030303u, x3 = (raw[0] >> 6) & 0x03030303u;
-      const uint32_t p = prmt(x0, x1, 0x5140), q = prmt(x2, x3, 0x5140);
-      const uint32_t r = prmt(x0, x1, 0x7362), t = prmt(x2, x3, 0x7362);
-      bytes_to_f16(prmt(p, q, 0x5410), 0xE402E402u, c);                 // -(1024 + 2)
-      bytes_to_f16(prmt(p, q, 0x7632), 0xE402E402u, c + 2);
-      bytes_to_f16(prmt(r, t, 0x5410), 0xE402E402u, c + 4);
-      bytes_to_f16(prmt(r, t, 0x7632), 0xE402E402u, c + 6);
-    }
-    if constexpr (!GROUP) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) hi[i] = c[i];
-    } else {
-      const uint32_t s2 = s | (s << 16);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        hi[i] = h2mul(c[i], s2);
-        if constexpr (LO) lo[i] = h2fma(c[i], s2, h2neg(hi[i]));   // exact but for f16 subnormals
-      }
-    }
-  }
-}
-
-// Non-finite elements of a row.  A token whose row holds one must not reach the queries that do
-// not see it, although its zero weight multiplies it there: it goes into the score operand as
-// NaN (every query that sees it becomes NaN) and into the output operand as zero.
-template <bool BF16>
-__device__ __forceinline__ bool nonfinite16(const uint32_t (&w)[8]) {
-  const uint32_t e = BF16 ? 0x7F807F80u : 0x7C007C00u;
-  uint32_t any = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t x = w[i] & e;   // a half equal to its exponent mask is inf or NaN
-    any |= ((x & 0xFFFFu) == (e & 0xFFFFu)) | ((x >> 16) == (e >> 16));
-  }
-  return any != 0;
-}
-template <bool BF16>
-__device__ __noinline__ void replace_nonfinite(uint32_t* w, uint32_t with) {
-  const uint32_t e = BF16 ? 0x7F80u : 0x7C00u;
-  for (int i = 0; i < 8; ++i) {
-    if ((w[i] & e) == e) w[i] = (w[i] & 0xFFFF0000u) | with;
-    if (((w[i] >> 16) & e) == e) w[i] = (w[i] & 0xFFFFu) | (with << 16);
-  }
-}
-
-template <int BITS, bool GROUP>
-struct Unit {
-  uint32_t w[kRaw<BITS>];
-  uint32_t s;
-};
-
-// 16 elements of row `slot` from element e (a multiple of 16) on; slot < 0: not read
-template <int BITS, bool GROUP>
-__device__ __forceinline__ void load_unit(const ChunkArgs& a, int slot, int e,
-                                          Unit<BITS, GROUP>& u) {
-  constexpr int RW = kRaw<BITS>;
-  if (slot < 0 || e < 0) return;
-  const uint8_t* p = a.codes + (int64_t)slot * a.row_bytes + e * kElemBits<BITS> / 8;
-  if constexpr (RW == 1) {
-    u.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-  } else if constexpr (RW == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    u.w[0] = v.x;
-    u.w[1] = v.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < RW / 4; ++i) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-      u.w[4 * i] = v.x;
-      u.w[4 * i + 1] = v.y;
-      u.w[4 * i + 2] = v.z;
-      u.w[4 * i + 3] = v.w;
-    }
-  }
-  if constexpr (GROUP)
-    u.s = __ldg(reinterpret_cast<const unsigned short*>(a.scales) + (int64_t)slot * a.sg +
-                e / a.group);
-}
 
 // Store 16 converted elements of atom row t, columns 16 sub .. 16 sub + 15 (two 16-byte chunks
 // under the 128-byte swizzle)
@@ -500,9 +348,10 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* buf, int64_t* 
   return before + x - v;
 }
 
-template <int BITS, bool GROUP>
+template <int BITS, bool GROUP, bool kExp>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-chunk_tc_kernel(const __grid_constant__ TcChunk P) {
+chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUtensorMap map_hi,
+                const __grid_constant__ CUtensorMap map_lo) {
   constexpr bool kBf16 = BITS == KVK_BITS_BF16;
   constexpr bool kTok = !GROUP && !kBf16;             // one scale per token
   constexpr bool kLo = kSplit<BITS, GROUP>;
@@ -519,22 +368,27 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P) {
     S.abort_word = 0;
     for (int i = 0; i < kTokStages; ++i) {
       mbar_init(&S.tok_full[i], 1);
-      mbar_init(&S.tok_empty[i], 12 + (rank == 0 ? 1 : 0));
+      mbar_init(&S.tok_empty[i], rank == 0 ? 14 : 13);
     }
     for (int i = 0; i < kMaxK; ++i) {
-      mbar_init(&S.k_full[i], 8);
+      mbar_init(&S.k_full[i], kExp ? 1 : 4);
+      mbar_init(&S.k_ready[i], 2);
       mbar_init(&S.k_empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&S.v_full[i], 8);
+      mbar_init(&S.v_land[i], 1);
+      mbar_init(&S.v_full[i], 4);
+      mbar_init(&S.v_ready[i], 2);
       mbar_init(&S.v_empty[i], 1);
-      mbar_init(&S.q_local[i], 8);
+      mbar_init(&S.q_local[i], kExp ? 7 : 8);
     }
-    mbar_init(&S.q_full, 16);
+    mbar_init(&S.q_full, kExp ? 7 : 8);
+    mbar_init(&S.q_ready, 2);
     mbar_init(&S.q_empty, 1);
     mbar_init(&S.s_full[0], 1);
     mbar_init(&S.s_full[1], 1);
-    mbar_init(&S.p_full, 8);
+    mbar_init(&S.p_full, 4);
+    mbar_init(&S.p_ready, 2);
     mbar_init(&S.pv_done, 1);
     mbar_init(&S.x_bar, 4);
     mbar_init(&S.drain, 1);
@@ -664,7 +518,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P) {
           }
           // the rows that this CTA converts for the scores are fetched into L2 now
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; !kExp && i < 2; ++i) {
             const int my = rank ? sl[2 + i] : sl[i];
             if (my >= 0)
               asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
@@ -672,7 +526,9 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P) {
                            "r"(a.row_bytes)
                            : "memory");
           }
-          float sc[4];
+          float sc[4], mk[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mk[i] = (kExp && sl[i] >= 0) ? __ldg(P.mark + sl[i]) : 0.0f;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             sc[i] = (kTok && sl[i] >= 0) ? __half2float(a.scales[sl[i]]) : 1.0f;
@@ -686,9 +542,9 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P) {
               const float w = sc[i] == 0.0f ? 5.9604644775390625e-8f : sc[i];
               T.sc[x] = sl[i] >= 0 ? sc[i] : 0.0f;
               T.isc[x] = sl[i] >= 0 ? 1.0f / w : 0.0f;
-              T.lsc[x] = sl[i] >= 0 ? log2f(w) : -CUDART_INF_F;
+              T.lsc[x] = sl[i] >= 0 ? log2f(w) + mk[i] : -CUDART_INF_F;
             } else {
-              T.lsc[x] = sl[i] >= 0 ? 0.0f : -CUDART_INF_F;
+              T.lsc[x] = sl[i] >= 0 ? mk[i] : -CUDART_INF_F;
             }
           }
           if (lane == 0) {
@@ -749,13 +605,12 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P) {
       bool first_prev = false;
       // output MMAs of block g (its first of a piece starts the sums anew)
       auto output = [&](int g, bool first) -> bool {
-        if (!wait(&S.p_full, g & 1)) return false;
-        tc_fence_after();
+        if (!wait(&S.p_ready, g & 1)) return false;
+        tc_fence_after();   // the softmax's reads of S and stores to O
         const int vs = g % P.NVS;
         const uint32_t vpar = (g / P.NVS) & 1;
         for (int ch = 0; ch < nch; ++ch) {
-          if (!wait(&S.v_full[vs * 2 + ch], vpar)) return false;
-          tc_fence_after();
+          if (!wait(&S.v_ready[vs * 2 + ch], vpar)) return false;
           const bool two = 2 * ch + 2 <= P.NV;
           const uint32_t idesc = two ? P.idesc_o2 : P.idesc_o1;
           const uint32_t hstep = (two ? 2 * kAtom : kAtom) >> 4;
@@ -780,17 +635,15 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P) {
         mbar_arrive(&S.tok_empty[st]);
         if (fl & kEnd) break;
         if (fl & kFirst) {
-          ok = wait(&S.q_full, pieces & 1);
+          ok = wait(&S.q_ready, pieces & 1);
           if (!ok) break;
-          tc_fence_after();
         }
         const uint32_t scol = tmem + kSCol + 64u * (g & 1);
         const int parts = kLo ? 2 : 1;
         for (int at = 0; ok && at < P.NA; ++at) {
           for (int part = 0; part < parts; ++part) {
-            ok = wait(&S.k_full[kslot], kpar);
+            ok = wait(&S.k_ready[kslot], kpar);
             if (!ok) break;
-            tc_fence_after();
             const uint64_t ad = q0 + ((uint32_t)at * kAtom >> 4);
             const uint64_t bd = kb0 + ((uint32_t)kslot * kAtom >> 4);
 #pragma unroll
@@ -822,10 +675,187 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P) {
           "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
               smem_u32(&S.drain))
           : "memory");
-      const uint64_t t0 = globaltimer();
-      while (!try_cl(&S.drain, 0u, 20000u) && globaltimer() - t0 < kDrainLimitNs) {
+      drain(&S.drain, 0u);
+    }
+  } else if (warp == kRelayWarp) {
+    // ======================= relay ==============================================================
+    // One thread passes this CTA's full barriers, in the order of the MMAs, on to the leader.  It
+    // makes the proxy fence for the threads that wrote the operands, whose own would wait for
+    // all their loads in flight (measured 1600 cycles per atom of the K team), and the MMA
+    // issuer's for its MMAs.
+    if (lane == 0) {
+      auto pass = [&](uint64_t* b, uint64_t* ready, uint32_t parity) -> bool {
+        if (!wait(b, parity)) return false;
+        fence_proxy_async_smem();
+        arrive_at(ready, 0);
+        return true;
+      };
+      auto output = [&](int g) -> bool {
+        if (!pass(&S.p_full, &S.p_ready, g & 1)) return false;
+        for (int ch = 0; ch < nch; ++ch) {
+          const int v = g % P.NVS * 2 + ch;
+          if (!pass(&S.v_full[v], &S.v_ready[v], (g / P.NVS) & 1)) return false;
+        }
+        return true;
+      };
+      int kslot = 0, pieces = 0, g = 0;
+      uint32_t kpar = 0;
+      bool ok = true;
+      for (;; ++g) {
+        const int st = g % kTokStages;
+        ok = wait(&S.tok_full[st], (g / kTokStages) & 1);
+        if (!ok) break;
+        const int fl = *const_cast<volatile int32_t*>(&S.tok[st].flags);
+        mbar_arrive(&S.tok_empty[st]);
+        if (fl & kEnd) break;
+        if (fl & kFirst) ok = pass(&S.q_full, &S.q_ready, pieces & 1);
+        if (fl & kLast) ++pieces;
+        for (int i = 0; ok && i < P.NA * (kLo ? 2 : 1); ++i) {
+          ok = pass(&S.k_full[kslot], &S.k_ready[kslot], kpar);
+          if (++kslot == P.NK) {
+            kslot = 0;
+            kpar ^= 1;
+          }
+        }
+        if (ok && g > 0) ok = output(g - 1);
+        if (!ok) break;
+      }
+      if (ok && g > 0) output(g - 1);
+    }
+  } else if (kExp && warp >= kVWarp0) {
+    // ======================= V loads (expanded rows) ============================================
+    // One thread loads the atoms; behind the last token the boxes hold whatever the rows there
+    // hold, so the team zeroes those rows before it passes the operand on.
+    const int vt = tid - kVWarp0 * 32, vw = warp - kVWarp0;
+    uint32_t armed = 0, landing = 0;                  // barriers used so far, and their last phase
+    bool ok = true;
+    for (int g = 0;; ++g) {
+      const int st = g % kTokStages;
+      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], (g / kTokStages) & 1));
+      if (!ok) break;
+      const TokStage& T = S.tok[st];
+      const int fl = T.flags;
+      if (fl & kEnd) break;
+      if (fl & kFirst) {
+        const QueryTile head = {T.row0, T.flat0, T.rows, T.piece};
+        if (head.piece > 0) ok = wait(&S.q_empty, (head.piece - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        stage_query<kBf16>(P, S, q_s, head, (int)rank, 32 + vw * 8, 32 + vw * 8 + 8);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&S.q_local[head.piece & 3]);
+          mbar_arrive(&S.q_full);
+        }
+      }
+      const int vs = g % P.NVS;
+      const uint32_t vpar = (g / P.NVS) & 1;
+      const uint32_t stage = P.off_v + (uint32_t)(vs * 2 * P.NV) * kAtom;
+      if (vw == 0) {
+        for (int ch = 0; ok && ch < nch; ++ch) {
+          const int nj = min(2, P.NV - 2 * ch);
+          ok = __all_sync(0xffffffffu, wait(&S.v_empty[vs * 2 + ch], vpar ^ 1));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&S.v_land[vs * 2 + ch], 2u * nj * kAtom);
+          armed |= 1u << (vs * 2 + ch);
+          landing = (landing & ~(1u << (vs * 2 + ch))) | vpar << (vs * 2 + ch);
+          __syncwarp();
+          // one box a lane: token row group, atom of the step
+          const int per = 128 / P.box;
+          for (int i = lane; i < per * nj; i += 32) {
+            const int jj = i / per, t = (i - jj * per) * P.box;
+            const int sl = T.slot[t];
+            const uint32_t at = stage + (uint32_t)(4 * ch + (t >> 6) * nj + jj) * kAtom +
+                                (uint32_t)(t & 63) * 128u;
+            tma_load_2d(smem + at, &map_hi, ((int)rank * P.NV + 2 * ch + jj) * 64,
+                        sl < 0 ? P.pool_slots : sl, &S.v_land[vs * 2 + ch]);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) break;
+      const int live = min(128, T.len - T.t0);       // rows that hold tokens
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.tok_empty[st]);
+      for (int ch = 0; ch < nch; ++ch) {
+        const int nj = min(2, P.NV - 2 * ch);
+        ok = __all_sync(0xffffffffu, wait(&S.v_land[vs * 2 + ch], vpar));
+        if (!ok) break;
+        if (live < 128) {                             // 8 lanes a row
+          for (int t = max(live, 0) + (vt >> 3); t < 128; t += 16)
+            for (int jj = 0; jj < nj; ++jj)
+              sts128(q_s + stage + (uint32_t)(4 * ch + (t >> 6) * nj + jj) * kAtom +
+                         (uint32_t)(t & 63) * 128u + (uint32_t)(vt & 7) * 16u,
+                     make_uint4(0u, 0u, 0u, 0u));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.v_full[vs * 2 + ch]);
+      }
+      if (!ok) break;
+    }
+    if (vw == 0 && lane == 0)
+      for (int j = 0; j < 4; ++j)
+        if (armed >> j & 1) drain(&S.v_land[j], landing >> j & 1);
+  } else if (kExp && warp >= kKWarp0) {
+    // ======================= K loads (expanded rows) ============================================
+    // Warp 4 loads; the other three stage query rows (a load may wait for MMAs that wait for
+    // them).
+    const int kw = warp - kKWarp0;
+    int kslot = 0;
+    uint32_t kpar = 1;
+    bool ok = true;
+    for (int g = 0;; ++g) {
+      const int st = g % kTokStages;
+      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], (g / kTokStages) & 1));
+      if (!ok) break;
+      const TokStage& T = S.tok[st];
+      const int fl = T.flags;
+      if (fl & kEnd) break;
+      if (kw == 0) {
+        const int per = 64 / P.box;
+        int sl = P.pool_slots;
+        if (lane < per) {
+          const int x = T.slot[64 * (int)rank + lane * P.box];
+          if (x >= 0) sl = x;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.tok_empty[st]);
+        for (int i = 0; i < P.NA * (kLo ? 2 : 1); ++i) {
+          const int at = kLo ? i >> 1 : i;
+          ok = __all_sync(0xffffffffu, wait(&S.k_empty[kslot], kpar));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&S.k_full[kslot], kAtom);
+          __syncwarp();
+          if (lane < per)
+            tma_load_2d(smem + P.off_k + (uint32_t)kslot * kAtom + (uint32_t)(lane * P.box) * 128u,
+                        (kLo && (i & 1)) ? &map_lo : &map_hi, at * 64, sl, &S.k_full[kslot]);
+          if (++kslot == P.NK) {
+            kslot = 0;
+            kpar ^= 1;
+          }
+        }
+        if (!ok) break;
+      } else {
+        const QueryTile head = {T.row0, T.flat0, T.rows, T.piece};
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.tok_empty[st]);
+        if (fl & kFirst) {
+          if (head.piece > 0) ok = wait(&S.q_empty, (head.piece - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const int r0 = kw == 1 ? 0 : kw == 2 ? 12 : 22;
+          stage_query<kBf16>(P, S, q_s, head, (int)rank, r0, kw == 1 ? 12 : r0 + 10);
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&S.q_local[head.piece & 3]);
+            mbar_arrive(&S.q_full);
+          }
+        }
       }
     }
+    // loads in flight land before the CTA's memory goes (only a stopped kernel has any)
+    if (kw == 0 && lane == 0)
+      for (int j = 0; j < P.NK; ++j) drain(&S.k_full[j], j < kslot ? kpar ^ 1 : kpar);
   } else if (warp >= kVWarp0) {
     // ======================= V team =============================================================
     const int vt = tid - kVWarp0 * 32, tq = vt >> 2, sub = vt & 3;
@@ -854,11 +884,10 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P) {
         if (!ok) break;
         const QueryTile head = {T.row0, T.flat0, T.rows, T.piece};
         stage_query<kBf16>(P, S, q_s, head, (int)rank, 32 + vw * 8, 32 + vw * 8 + 8);
-        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&S.q_local[T.piece & 3]);
-          arrive_at(&S.q_full, 0);
+          mbar_arrive(&S.q_full);
         }
       }
       __syncwarp();
@@ -897,9 +926,8 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P) {
           }
         }
         if (!ok) break;
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) arrive_at(&S.v_full[vs * 2 + ch], 0);
+        if (lane == 0) mbar_arrive(&S.v_full[vs * 2 + ch]);
       }
       if (!ok) break;
     }
@@ -968,11 +996,10 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P) {
       if (piece > 0) ok = __all_sync(0xffffffffu, wait(&S.q_empty, (piece - 1) & 1));
       if (!ok) break;
       stage_query<kBf16>(P, S, q_s, head, (int)rank, kw * 8, kw * 8 + 8);
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&S.q_local[piece & 3]);
-        arrive_at(&S.q_full, 0);
+        mbar_arrive(&S.q_full);
       }
       bool done = false;
       while (!done) {
@@ -1008,9 +1035,8 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P) {
             const uint32_t atom = k_s + (uint32_t)kslot * kAtom;
 #pragma unroll
             for (int u = 0; u < 2; ++u) store_unit(atom, tq + 32 * u, sub, part ? lo[u] : hi[u]);
-            fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) arrive_at(&S.k_full[kslot], 0);
+            if (lane == 0) mbar_arrive(&S.k_full[kslot]);
             if (++kslot == P.NK) {
               kslot = 0;
               kpar ^= 1;
@@ -1158,10 +1184,9 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P) {
           sts128(row + (uint32_t)((c ^ (r & 7)) << 4),
                  make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]));
       }
-      fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_at(&S.p_full, 0);
+      if (lane == 0) mbar_arrive(&S.p_full);
       if (!last) continue;
 
       // ---- the piece's output ----
@@ -1294,12 +1319,39 @@ __host__ constexpr uint32_t idesc_of(bool bf16, int N, bool b_mn) {
   return idesc_f16(128, N, false, b_mn) | (bf16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
-template <int BITS, bool GROUP>
-cudaError_t launch(const TcChunk& P, size_t smem, cudaStream_t st) {
-  auto k = chunk_tc_kernel<BITS, GROUP>;
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The expanded rows as a 2D tensor [slots][64 NA] of 16-bit elements; box = one atom's 64
+// features x `rows` slots, 128-byte swizzle.  Rows behind the pool read as zero.
+bool expanded_map(CUtensorMap* m, void* base, int NA, int64_t slots, int rows) {
+  static EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)NA * 64, (cuuint64_t)slots};
+  const cuuint64_t strides[1] = {(cuuint64_t)NA * 128};
+  const cuuint32_t box[2] = {64, (cuuint32_t)rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BITS, bool GROUP, bool kExp>
+cudaError_t launch(const TcChunk& P, const CUtensorMap& hi, const CUtensorMap& lo, size_t smem,
+                   cudaStream_t st) {
+  auto k = chunk_tc_kernel<BITS, GROUP, kExp>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  k<<<dim3(2 * P.w.G), dim3(kThreads), smem, st>>>(P);
+  k<<<dim3(2 * P.w.G), dim3(kThreads), smem, st>>>(P, hi, lo);
   return cudaGetLastError();
 }
 
@@ -1317,8 +1369,8 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkWork& w, int dtype, c
   memset(&P, 0, sizeof(P));
   P.a = a;
   P.w = w;
-  P.NL = (a.d + 127) / 128 * 2;
-  P.NA = P.NL + (a.d_rope + 63) / 64;
+  P.NL = latent_atoms(a.d);
+  P.NA = row_atoms(a.d, a.d_rope);
   P.NV = P.NL / 2;
   P.NVS = P.NV <= 2 ? 2 : 1;
   const int room = (int)((kSmemLimit - (int)sizeof(Shared)) / (int)kAtom) - P.NA - 2 * P.NV * P.NVS - 2;
@@ -1336,38 +1388,71 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkWork& w, int dtype, c
   // the prologue's prefix sums use the rings' memory
   if (P.NK < 2 || smem > (size_t)kSmemLimit || (size_t)(a.batch + 1) * 4 > P.off_misc)
     return cudaErrorInvalidValue;
+  CUtensorMap hi, lo;
+  memset(&hi, 0, sizeof(hi));
+  memset(&lo, 0, sizeof(lo));
   cudaError_t e = cudaErrorInvalidValue;
-  if (a.group) {
-    if (a.b == 2) e = launch<2, true>(P, smem, st);
-    else if (a.b == 4) e = launch<4, true>(P, smem, st);
-    else if (a.b == 8) e = launch<8, true>(P, smem, st);
-    else if (a.b == 16) e = launch<16, true>(P, smem, st);
+  if (w.hi) {
+    const bool split = chunk_split(a.b, a.group);
+    P.mark = w.mark;
+    P.box = std::min(1 << a.page_shift, 64);
+    P.pool_slots = w.pool_slots;
+    if (!expanded_map(&hi, w.hi, P.NA, w.pool_slots, P.box) ||
+        (split && !expanded_map(&lo, w.lo, P.NA, w.pool_slots, P.box)))
+      return cudaErrorInvalidValue;
+    e = launch_chunk_expand(a, w, st);
+    if (e != cudaSuccess) return e;
+    // (the operands' form does not depend on the width of the codes any more)
+    if (bf) e = launch<KVK_BITS_BF16, false, true>(P, hi, lo, smem, st);
+    else if (a.group) e = launch<8, true, true>(P, hi, lo, smem, st);
+    else if (split) e = launch<16, false, true>(P, hi, lo, smem, st);
+    else e = launch<8, false, true>(P, hi, lo, smem, st);
+  } else if (a.group) {
+    if (a.b == 2) e = launch<2, true, false>(P, hi, lo, smem, st);
+    else if (a.b == 4) e = launch<4, true, false>(P, hi, lo, smem, st);
+    else if (a.b == 8) e = launch<8, true, false>(P, hi, lo, smem, st);
+    else if (a.b == 16) e = launch<16, true, false>(P, hi, lo, smem, st);
   } else {
-    if (a.b == KVK_BITS_BF16) e = launch<KVK_BITS_BF16, false>(P, smem, st);
-    else if (a.b == 2) e = launch<2, false>(P, smem, st);
-    else if (a.b == 4) e = launch<4, false>(P, smem, st);
-    else if (a.b == 8) e = launch<8, false>(P, smem, st);
-    else if (a.b == 16) e = launch<16, false>(P, smem, st);
+    if (bf) e = launch<KVK_BITS_BF16, false, false>(P, hi, lo, smem, st);
+    else if (a.b == 2) e = launch<2, false, false>(P, hi, lo, smem, st);
+    else if (a.b == 4) e = launch<4, false, false>(P, hi, lo, smem, st);
+    else if (a.b == 8) e = launch<8, false, false>(P, hi, lo, smem, st);
+    else if (a.b == 16) e = launch<16, false, false>(P, hi, lo, smem, st);
   }
   if (e != cudaSuccess) return e;
   chunk_merge_kernel<<<dim3(w.G, 128 / kMergeWarps), dim3(kMergeWarps * 32), 0, st>>>(a, w, P.q_bf16);
   return cudaGetLastError();
 }
 
-size_t chunk_workspace(int d, int G, void* base, ChunkWork* w) {
+size_t chunk_workspace(const AnchorDesc& A, int d_rope, int group, int64_t slots, int G, bool expand,
+                       void* base, ChunkWork* w) {
   size_t off = 0;
   const size_t o_head = off;
   off = align_up_sz(off + sizeof(ChunkPartial) * 2 * (size_t)G, 256);
   const size_t o_ml = off;
   off = align_up_sz(off + sizeof(float) * 2 * 128 * 2 * (size_t)G, 256);
   const size_t o_o = off;
-  off = align_up_sz(off + sizeof(float) * (size_t)d * 128 * 2 * (size_t)G, 256);
+  off = align_up_sz(off + sizeof(float) * (size_t)A.d * 128 * 2 * (size_t)G, 256);
+  const size_t plane = (size_t)slots * row_atoms(A.d, d_rope) * 128;
+  const bool split = chunk_split(A.b, group);
+  size_t o_mark = off, o_hi = off, o_lo = off;
+  if (expand) {
+    off = align_up_sz(off + sizeof(float) * (size_t)slots, 256);
+    o_hi = off;
+    off = align_up_sz(off + plane, 256);
+    o_lo = off;
+    if (split) off = align_up_sz(off + plane, 256);
+  }
   if (base && w) {
     uint8_t* p = static_cast<uint8_t*>(base);
     w->head = reinterpret_cast<ChunkPartial*>(p + o_head);
     w->ml = reinterpret_cast<float*>(p + o_ml);
     w->o = reinterpret_cast<float*>(p + o_o);
     w->G = G;
+    w->mark = expand ? reinterpret_cast<float*>(p + o_mark) : nullptr;
+    w->hi = expand ? p + o_hi : nullptr;
+    w->lo = expand && split ? p + o_lo : nullptr;
+    w->pool_slots = (int)slots;
   }
   return off;
 }

@@ -44,6 +44,19 @@ int chunk_path(const kvk_layout* L, const AnchorDesc& A, int dtype) {
   return kvk::chunk_fma_fits(A.n) ? KVK_PATH_CUDA_CORE : -1;
 }
 
+// Whether a call's rows are converted once ahead of the attention (kvk_chunk_expand.cu) instead
+// of in every row tile: from kExpandTiles row tiles per sequence on, over the batch.
+constexpr int kExpandTiles = 3;
+bool expand_pays(int n_q, int batch, int n_heads) {
+  return (int64_t)n_q * n_heads >= (int64_t)kExpandTiles * 128 * batch;
+}
+
+size_t chunk_bytes(const kvk_layout* L, const AnchorDesc& A, bool expand, void* base,
+                   kvk::ChunkWork* w) {
+  return kvk::chunk_workspace(A, L->d_rope, kvk::anchor_group(L, A), pool_slots(L),
+                              chunk_clusters(L), expand, base, w);
+}
+
 bool known_dtype(int t) { return t == KVK_F32 || t == KVK_BF16 || t == KVK_F16; }
 
 }  // namespace
@@ -138,7 +151,8 @@ kvk_status kvk_chunk_workspace_bytes(const kvk_layout* L, int layer, int n_q, in
   if (!L || !bytes || layer < 0 || layer >= L->n_layers || n_q < 0 || batch < 1 ||
       batch > kvk::kMaxPagedBatch || n_heads < 1 || n_heads > 4096)
     return KVK_ERR_INVALID_ARG;
-  *bytes = kvk::chunk_workspace(L->anchors[L->slot[layer]].d, chunk_clusters(L), nullptr, nullptr);
+  const AnchorDesc& A = L->anchors[L->slot[layer]];
+  *bytes = chunk_bytes(L, A, expand_pays(n_q, batch, n_heads), nullptr, nullptr);
   return KVK_OK;
 }
 
@@ -216,8 +230,10 @@ kvk_status kvk_mla_chunk(kvk_layout* L, int layer, const void* q_lat, const void
   if (path == KVK_PATH_TENSOR) {
     kvk::ChunkWork w;
     memset(&w, 0, sizeof(w));
-    if (workspace_bytes < kvk::chunk_workspace(A.d, chunk_clusters(L), workspace, &w))
-      return KVK_ERR_WORKSPACE;
+    // a box of expanded rows is 8 rows at least (the swizzle's period) and lies in one page
+    const bool expand = expand_pays(n_q, batch, n_heads) && page_tokens >= 8 &&
+                        workspace_bytes >= chunk_bytes(L, A, true, nullptr, nullptr);
+    if (workspace_bytes < chunk_bytes(L, A, expand, workspace, &w)) return KVK_ERR_WORKSPACE;
     e = kvk::launch_chunk_tc(a, w, dtype, st);
   } else {
     e = kvk::launch_chunk_fma(a, dtype, st);

@@ -295,6 +295,11 @@ CHUNKS = {   # lens, q_lens, heads, page
     "empty": ([0, 0], [2, 0], 4, 16),
     "many_heads": ([150], [3], 130, 1),
     "one_head": ([140], [140], 1, 256),
+    # many row tiles a sequence: rows expanded once ahead of the attention
+    "prefill": ([300, 129, 64], [300, 129, 64], 8, 16),
+    "late_chunk": ([1000, 70], [130, 70], 12, 64),
+    "small_pages": ([450], [100], 16, 8),
+    "tiny_pages": ([450], [100], 16, 4),
 }
 
 
@@ -318,12 +323,13 @@ def test_chunk_matches_reference(pkg, oracle_mod, path, case, b, G):
 SHAPES = [(512, 64), (384, 64), (256, 64), (16, 16), (192, 32), (512, 0), (80, 48)]
 
 
+@pytest.mark.parametrize("q_lens", [[40, 1, 9], [100, 64, 120]], ids=["few", "many"])
 @pytest.mark.parametrize("d,dR", SHAPES)
 @pytest.mark.parametrize("dtype,b", [(torch.bfloat16, 16), (torch.bfloat16, 8), (torch.float16, 4),
                                      (torch.bfloat16, BF16_ROWS), (torch.float16, 16),
                                      (torch.float32, 16)])
-def test_chunk_shapes_and_types(pkg, oracle_mod, d, dR, dtype, b):
-    lens, q_lens, H = [333, 64, 700], [40, 1, 9], 7
+def test_chunk_shapes_and_types(pkg, oracle_mod, d, dR, dtype, b, q_lens):
+    lens, H = [333, 64, 700], 7
     pool = Pool(pkg, oracle_mod, lens, d, dR, b, 0, 32, d + b)
     try:
         sigma = 1 / math.sqrt(d + dR)
