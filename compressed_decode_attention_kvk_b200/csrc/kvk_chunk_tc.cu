@@ -22,7 +22,7 @@
 //   4-7    K team: own 64 tokens, packed codes -> 16-bit operand atoms (64 tokens x 64 features,
 //          128-byte swizzle) of a ring that the score MMA drains
 //   8-11   V team: all 128 tokens, this CTA's half of the latent features, for the output MMA
-//   12     MMA issuer (one thread of the leader CTA)
+//   12     MMA issuer (the leader CTA's)
 //   13     token warp: walks the cluster's pieces, resolves pages to slots, loads token scales,
 //          warms L2 with the rows, four blocks ahead of the others
 //   14     relay: passes the barriers of written operands on to the leader
@@ -151,21 +151,32 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-// Arrives on the barrier of both CTAs once this thread's MMAs so far are complete.
+// Arrives on the barrier of both CTAs once the elected lane's MMAs so far are complete.
 __device__ __forceinline__ void commit_both(uint64_t* bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;\n\t}" ::"r"(smem_u32(bar)),
       "h"((uint16_t)3)
       : "memory");
 }
-__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                     uint32_t acc) {
+// Four MMAs of the pair, D (+)= A_k B_k, issued by the elected lane of a converged warp: with the
+// descriptors in uniform registers the pattern of one block (36 score and 16 output MMAs) takes
+// 2380 cycles with its commits (2176 at the full rate); a lone thread issuing them took 6500.
+__device__ __forceinline__ void mma2x4(uint32_t d, uint64_t a, uint64_t b, uint32_t b_step,
+                                       uint32_t idesc, uint32_t acc) {
+  const uint64_t a1 = a + 2, a2 = a + 4, a3 = a + 6;      // K steps of 16: 32 bytes
+  const uint64_t b1 = b + b_step, b2 = b + 2u * b_step, b3 = b + 3u * b_step;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %10, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %5, %9, p;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %2, %6, %9, 1;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %3, %7, %9, 1;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %4, %8, %9, 1;\n\t}" ::"r"(d),
+      "l"(a), "l"(a1), "l"(a2), "l"(a3), "l"(b), "l"(b1), "l"(b2), "l"(b3), "r"(idesc), "r"(acc)
       : "memory");
 }
 // 32 lanes x 32 columns: thread i of the warp holds lane base + i
@@ -595,7 +606,10 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     }
   } else if (warp == kMmaWarp) {
     // ======================= MMA issuer =========================================================
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {   // the whole warp, converged
+      auto all = [&](uint64_t* b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, wait(b, parity));
+      };
       const uint64_t q0 = sdesc(q_s, 16u, 1024u, kLayoutSw128);
       const uint64_t kb0 = sdesc(k_s, 16u, 1024u, kLayoutSw128);
       const uint64_t p0 = sdesc(p_s, 16u, 1024u, kLayoutSw128);
@@ -605,21 +619,19 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       bool first_prev = false;
       // output MMAs of block g (its first of a piece starts the sums anew)
       auto output = [&](int g, bool first) -> bool {
-        if (!wait(&S.p_ready, g & 1)) return false;
+        if (!all(&S.p_ready, g & 1)) return false;
         tc_fence_after();   // the softmax's reads of S and stores to O
         const int vs = g % P.NVS;
         const uint32_t vpar = (g / P.NVS) & 1;
         for (int ch = 0; ch < nch; ++ch) {
-          if (!wait(&S.v_ready[vs * 2 + ch], vpar)) return false;
+          if (!all(&S.v_ready[vs * 2 + ch], vpar)) return false;
           const bool two = 2 * ch + 2 <= P.NV;
           const uint32_t idesc = two ? P.idesc_o2 : P.idesc_o1;
           const uint32_t hstep = (two ? 2 * kAtom : kAtom) >> 4;
           const uint64_t vb = vb0 + ((uint32_t)(vs * 2 * P.NV + 4 * ch) * kAtom >> 4);
           const uint32_t dcol = tmem + 128u * ch;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma2(dcol, p0 + (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2,
-                 vb + (kk >> 2) * hstep + (kk & 3) * 128, idesc, (kk > 0 || !first) ? 1u : 0u);
+          mma2x4(dcol, p0, vb, 128u, idesc, first ? 0u : 1u);
+          mma2x4(dcol, p0 + (kAtom >> 4), vb + hstep, 128u, idesc, 1u);
           commit_both(&S.v_empty[vs * 2 + ch]);
         }
         commit_both(&S.pv_done);
@@ -629,27 +641,25 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       int g = 0, pieces = 0;
       for (;; ++g) {
         const int st = g % kTokStages;
-        ok = wait(&S.tok_full[st], (g / kTokStages) & 1);
+        ok = all(&S.tok_full[st], (g / kTokStages) & 1);
         if (!ok) break;
         const int fl = *const_cast<volatile int32_t*>(&S.tok[st].flags);
-        mbar_arrive(&S.tok_empty[st]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.tok_empty[st]);
         if (fl & kEnd) break;
         if (fl & kFirst) {
-          ok = wait(&S.q_ready, pieces & 1);
+          ok = all(&S.q_ready, pieces & 1);
           if (!ok) break;
         }
         const uint32_t scol = tmem + kSCol + 64u * (g & 1);
         const int parts = kLo ? 2 : 1;
         for (int at = 0; ok && at < P.NA; ++at) {
           for (int part = 0; part < parts; ++part) {
-            ok = wait(&S.k_ready[kslot], kpar);
+            ok = all(&S.k_ready[kslot], kpar);
             if (!ok) break;
             const uint64_t ad = q0 + ((uint32_t)at * kAtom >> 4);
             const uint64_t bd = kb0 + ((uint32_t)kslot * kAtom >> 4);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma2(scol, ad + kk * 2, bd + kk * 2, P.idesc_s,
-                   (at > 0 || part > 0 || kk > 0) ? 1u : 0u);
+            mma2x4(scol, ad, bd, 2u, P.idesc_s, (at > 0 || part > 0) ? 1u : 0u);
             commit_both(&S.k_empty[kslot]);
             if (++kslot == P.NK) {
               kslot = 0;
@@ -671,10 +681,8 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       }
       if (ok && g > 0) ok = output(g - 1, first_prev);
       // every MMA and its arrivals are done before either CTA leaves
-      asm volatile(
-          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-              smem_u32(&S.drain))
-          : "memory");
+      __syncwarp();
+      commit_both(&S.drain);
       drain(&S.drain, 0u);
     }
   } else if (warp == kRelayWarp) {
