@@ -16,7 +16,7 @@
 // chunk_merge_kernel; a cluster owns at most two partial tiles, its first and its last, so the
 // workspace does not grow with the batch.
 //
-// Warps of a CTA (480 threads):
+// Warps of a CTA (512 threads):
 //   0-3    softmax: a row and 64 tokens a thread; S from TMEM, P (16 bit) to shared memory, O
 //          rescaled when a row's reference grows by more than 2^8, outputs
 //   4-7    K team: own 64 tokens, packed codes -> 16-bit operand atoms (64 tokens x 64 features,
@@ -24,7 +24,7 @@
 //   8-11   V team: all 128 tokens, this CTA's half of the latent features, for the output MMA
 //   12     MMA issuer (the leader CTA's)
 //   13     token warp: walks the cluster's pieces, resolves pages to slots, loads token scales,
-//          warms L2 with the rows, four blocks ahead of the others
+//          warms L2 with the rows, up to three blocks ahead of the others
 //   14     relay: passes the barriers of written operands on to the leader
 // Both teams stage the query rows at a piece's start.
 //
@@ -55,11 +55,11 @@ namespace {
 using namespace sm100;
 using namespace chunk;
 
-constexpr int kThreads = 480;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kKWarp0 = 4, kVWarp0 = 8, kMmaWarp = 12, kTokWarp = 13, kRelayWarp = 14;
+constexpr int kKWarp0 = 4, kVWarp0 = 8, kMmaWarp = 12, kTokWarp = 13, kRelayWarp = 14, kLoadWarp = 15;
 constexpr uint32_t kAtom = 8192;       // 64 rows x 128 bytes
-constexpr int kTokStages = 4;
+constexpr int kTokStages = 3;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;        // S buffers at 256 and 320 (64 columns); O at 0
 constexpr float kLog2e = 1.4426950408889634f;
@@ -86,8 +86,7 @@ constexpr int kEnd = 1, kFirst = 2, kLast = 4;
 struct Shared {
   TokStage tok[kTokStages];
   int8_t qexp[4][64];                  // per row: e of its query's scaling 2^e
-  float xch[2][128];                   // row maxima of the two token halves
-  float xl[128];
+  float xch[2][256];                   // maxima (at a piece's end: sums) of a row's threads
   uint64_t tok_full[kTokStages], tok_empty[kTokStages];
   // operands: written (by this CTA's warps), passed on (to the leader, by both relays), free
   uint64_t k_full[kMaxK], k_ready[kMaxK], k_empty[kMaxK];
@@ -366,6 +365,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
   constexpr bool kBf16 = BITS == KVK_BITS_BF16;
   constexpr bool kTok = !GROUP && !kBf16;             // one scale per token
   constexpr bool kLo = kSplit<BITS, GROUP>;
+  constexpr int kSoftWarps = kExp ? 8 : 4;
   extern __shared__ __align__(1024) uint8_t smem[];
   const ChunkArgs& a = P.a;
   Shared& S = *reinterpret_cast<Shared*>(smem + P.off_misc);
@@ -379,7 +379,8 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     S.abort_word = 0;
     for (int i = 0; i < kTokStages; ++i) {
       mbar_init(&S.tok_full[i], 1);
-      mbar_init(&S.tok_empty[i], rank == 0 ? 14 : 13);
+      // softmax warps, converting or loading warps, relay, the leader's MMA warp
+      mbar_init(&S.tok_empty[i], kSoftWarps + (kExp ? 5 : 8) + 1 + (rank == 0 ? 1 : 0));
     }
     for (int i = 0; i < kMaxK; ++i) {
       mbar_init(&S.k_full[i], kExp ? 1 : 4);
@@ -391,17 +392,17 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       mbar_init(&S.v_full[i], 4);
       mbar_init(&S.v_ready[i], 2);
       mbar_init(&S.v_empty[i], 1);
-      mbar_init(&S.q_local[i], kExp ? 7 : 8);
+      mbar_init(&S.q_local[i], kExp ? 4 : 8);
     }
-    mbar_init(&S.q_full, kExp ? 7 : 8);
+    mbar_init(&S.q_full, kExp ? 4 : 8);
     mbar_init(&S.q_ready, 2);
     mbar_init(&S.q_empty, 1);
     mbar_init(&S.s_full[0], 1);
     mbar_init(&S.s_full[1], 1);
-    mbar_init(&S.p_full, 4);
+    mbar_init(&S.p_full, kSoftWarps);
     mbar_init(&S.p_ready, 2);
     mbar_init(&S.pv_done, 1);
-    mbar_init(&S.x_bar, 4);
+    mbar_init(&S.x_bar, kSoftWarps);
     mbar_init(&S.drain, 1);
     fence_mbar_init();
     // no partials of this cluster yet
@@ -730,6 +731,41 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       }
       if (ok && g > 0) output(g - 1);
     }
+  } else if (warp == kLoadWarp) {
+    // ======================= K loads (expanded rows) ============================================
+    int kslot = 0;
+    uint32_t kpar = 1;
+    bool ok = kExp;
+    for (int g = 0; ok; ++g) {
+      const int st = g % kTokStages;
+      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], (g / kTokStages) & 1));
+      if (!ok || (S.tok[st].flags & kEnd)) break;
+      const int per = 64 / P.box;
+      int sl = P.pool_slots;
+      if (lane < per) {
+        const int x = S.tok[st].slot[64 * (int)rank + lane * P.box];
+        if (x >= 0) sl = x;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.tok_empty[st]);
+      for (int i = 0; i < P.NA * (kLo ? 2 : 1); ++i) {
+        const int at = kLo ? i >> 1 : i;
+        ok = __all_sync(0xffffffffu, wait(&S.k_empty[kslot], kpar));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&S.k_full[kslot], kAtom);
+        __syncwarp();
+        if (lane < per)
+          tma_load_2d(smem + P.off_k + (uint32_t)kslot * kAtom + (uint32_t)(lane * P.box) * 128u,
+                      (kLo && (i & 1)) ? &map_lo : &map_hi, at * 64, sl, &S.k_full[kslot]);
+        if (++kslot == P.NK) {
+          kslot = 0;
+          kpar ^= 1;
+        }
+      }
+    }
+    // loads in flight land before the CTA's memory goes (only a stopped kernel has any)
+    if (kExp && lane == 0)
+      for (int j = 0; j < P.NK; ++j) drain(&S.k_full[j], j < kslot ? kpar ^ 1 : kpar);
   } else if (kExp && warp >= kVWarp0) {
     // ======================= V loads (expanded rows) ============================================
     // One thread loads the atoms; behind the last token the boxes hold whatever the rows there
@@ -749,7 +785,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         if (head.piece > 0) ok = wait(&S.q_empty, (head.piece - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        stage_query<kBf16>(P, S, q_s, head, (int)rank, 32 + vw * 8, 32 + vw * 8 + 8);
+        stage_query<kBf16>(P, S, q_s, head, (int)rank, vw * 16, vw * 16 + 16);
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&S.q_local[head.piece & 3]);
@@ -804,67 +840,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     if (vw == 0 && lane == 0)
       for (int j = 0; j < 4; ++j)
         if (armed >> j & 1) drain(&S.v_land[j], landing >> j & 1);
-  } else if (kExp && warp >= kKWarp0) {
-    // ======================= K loads (expanded rows) ============================================
-    // Warp 4 loads; the other three stage query rows (a load may wait for MMAs that wait for
-    // them).
-    const int kw = warp - kKWarp0;
-    int kslot = 0;
-    uint32_t kpar = 1;
-    bool ok = true;
-    for (int g = 0;; ++g) {
-      const int st = g % kTokStages;
-      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], (g / kTokStages) & 1));
-      if (!ok) break;
-      const TokStage& T = S.tok[st];
-      const int fl = T.flags;
-      if (fl & kEnd) break;
-      if (kw == 0) {
-        const int per = 64 / P.box;
-        int sl = P.pool_slots;
-        if (lane < per) {
-          const int x = T.slot[64 * (int)rank + lane * P.box];
-          if (x >= 0) sl = x;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.tok_empty[st]);
-        for (int i = 0; i < P.NA * (kLo ? 2 : 1); ++i) {
-          const int at = kLo ? i >> 1 : i;
-          ok = __all_sync(0xffffffffu, wait(&S.k_empty[kslot], kpar));
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&S.k_full[kslot], kAtom);
-          __syncwarp();
-          if (lane < per)
-            tma_load_2d(smem + P.off_k + (uint32_t)kslot * kAtom + (uint32_t)(lane * P.box) * 128u,
-                        (kLo && (i & 1)) ? &map_lo : &map_hi, at * 64, sl, &S.k_full[kslot]);
-          if (++kslot == P.NK) {
-            kslot = 0;
-            kpar ^= 1;
-          }
-        }
-        if (!ok) break;
-      } else {
-        const QueryTile head = {T.row0, T.flat0, T.rows, T.piece};
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.tok_empty[st]);
-        if (fl & kFirst) {
-          if (head.piece > 0) ok = wait(&S.q_empty, (head.piece - 1) & 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const int r0 = kw == 1 ? 0 : kw == 2 ? 12 : 22;
-          stage_query<kBf16>(P, S, q_s, head, (int)rank, r0, kw == 1 ? 12 : r0 + 10);
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&S.q_local[head.piece & 3]);
-            mbar_arrive(&S.q_full);
-          }
-        }
-      }
-    }
-    // loads in flight land before the CTA's memory goes (only a stopped kernel has any)
-    if (kw == 0 && lane == 0)
-      for (int j = 0; j < P.NK; ++j) drain(&S.k_full[j], j < kslot ? kpar ^ 1 : kpar);
-  } else if (warp >= kVWarp0) {
+  } else if (!kExp && warp >= kVWarp0) {
     // ======================= V team =============================================================
     const int vt = tid - kVWarp0 * 32, tq = vt >> 2, sub = vt & 3;
     const int vw = warp - kVWarp0;
@@ -939,7 +915,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       }
       if (!ok) break;
     }
-  } else if (warp >= kKWarp0) {
+  } else if (!kExp && warp >= kKWarp0) {
     // ======================= K team =============================================================
     constexpr int D = 3;   // atoms whose loads are in flight
     const int kt = tid - kKWarp0 * 32, tq = kt >> 2, sub = kt & 3;
@@ -1058,15 +1034,21 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     }
   } else {
     // ======================= softmax ============================================================
-    const int r = tid & 63, hh = tid >> 6;          // row of the CTA, token half
-    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+    // A row belongs to one thread per token half and, with expanded rows, column group: the
+    // converting warps' place is then taken by a second set of softmax warps.
+    constexpr int kCols = kExp ? 32 : 64;            // S columns (tokens) of a thread
+    const int r = tid & 63, hh = (tid >> 6) & 1, cg = tid >> 7;
+    const int col0 = 64 * hh + kCols * cg;           // first token of the block
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const int oc = P.NV * 64;                        // O columns (features of one half)
+    const int ocg = kExp ? oc / 2 : oc;              // and those of this thread
+    const uint32_t obase = tmem + (uint32_t)(ocg * cg) + lanes;
     float m = -CUDART_INF_F, l = 0.0f, rc = 0.0f;
     int lim = 0, row_q = 0, row_h = 0;
     bool row_ok = false;
     bool ok = true;
     uint32_t met = 0;
-    auto meet = [&]() -> bool {                      // the four warps, bounded like every wait
+    auto meet = [&]() -> bool {                      // the softmax warps, bounded like every wait
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.x_bar);
       return __all_sync(0xffffffffu, wait(&S.x_bar, met++ & 1));
@@ -1096,18 +1078,18 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       ok = __all_sync(0xffffffffu, wait(&S.s_full[g & 1], (g >> 1) & 1));
       if (!ok) break;
       tc_fence_after();
-      float s[64];
-      const uint32_t sb = tmem + kSCol + 64u * (g & 1) + lanes;
-      tmem_ld32(sb, s);
-      tmem_ld32(sb + 32, s + 32);
+      float s[kCols];
+      const uint32_t sb = tmem + kSCol + 64u * (g & 1) + (uint32_t)(kCols * cg) + lanes;
+#pragma unroll
+      for (int i = 0; i < kCols; i += 32) tmem_ld32(sb + i, s + i);
       tmem_wait_ld();
       // w_t = z_t + log2 s_t, and its maximum over this half
-      const float4* lsc4 = reinterpret_cast<const float4*>(T.lsc + 64 * hh);
-      const float4* sc4 = reinterpret_cast<const float4*>(T.sc + 64 * hh);
-      const int vis = lim - T.t0 - 64 * hh;          // columns that the row sees
+      const float4* lsc4 = reinterpret_cast<const float4*>(T.lsc + col0);
+      const float4* sc4 = reinterpret_cast<const float4*>(T.sc + col0);
+      const int vis = lim - T.t0 - col0;             // columns that the row sees
       float mx = -CUDART_INF_F;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < kCols / 4; ++i) {
         const float4 b = lsc4[i];
         float4 c = make_float4(1.f, 1.f, 1.f, 1.f);
         if constexpr (kTok) c = sc4[i];
@@ -1119,16 +1101,18 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
           s[4 * i + k] = fmaf(z, rc, bb[k]);
         }
       }
-      if (__any_sync(0xffffffffu, vis < 64)) {
+      if (__any_sync(0xffffffffu, vis < kCols)) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) s[i] = i < vis ? s[i] : -CUDART_INF_F;
+        for (int i = 0; i < kCols; ++i) s[i] = i < vis ? s[i] : -CUDART_INF_F;
       }
 #pragma unroll
-      for (int i = 0; i < 64; ++i) mx = fmaxf(mx, s[i]);
+      for (int i = 0; i < kCols; ++i) mx = fmaxf(mx, s[i]);
       S.xch[g & 1][tid] = mx;
       ok = meet();
       if (!ok) break;
       mx = fmaxf(mx, S.xch[g & 1][tid ^ 64]);
+      if constexpr (kExp)
+        mx = fmaxf(mx, fmaxf(S.xch[g & 1][tid ^ 128], S.xch[g & 1][tid ^ 192]));
       float alpha = 1.0f;
       if (mx > m + kLazy) {
         alpha = exp2f(m - mx);   // m = -inf: 0
@@ -1136,11 +1120,11 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         m = mx;
       }
       const float mref = m == -CUDART_INF_F ? 0.0f : m;
-      uint32_t pk[32];
-      const float4* isc4 = reinterpret_cast<const float4*>(T.isc + 64 * hh);
+      uint32_t pk[kCols / 2];
+      const float4* isc4 = reinterpret_cast<const float4*>(T.isc + col0);
       float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < kCols / 4; ++i) {
         float4 c = make_float4(1.f, 1.f, 1.f, 1.f);
         if constexpr (kTok) c = isc4[i];
         const float cc[4] = {c.x, c.y, c.z, c.w};
@@ -1175,21 +1159,21 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         tc_fence_after();
       }
       if (!(fl & kFirst) && __any_sync(0xffffffffu, alpha != 1.0f)) {
-        for (int c = 0; c < oc; c += 32) {
+        for (int c = 0; c < ocg; c += 32) {
           float o[32];
-          tmem_ld32(tmem + c + lanes, o);
+          tmem_ld32(obase + c, o);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] *= alpha;
-          tmem_st32(tmem + c + lanes, o);
+          tmem_st32(obase + c, o);
         }
         tmem_wait_st();
       }
       {
         const uint32_t row = p_s + (uint32_t)hh * kAtom + (uint32_t)r * 128u;
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          sts128(row + (uint32_t)((c ^ (r & 7)) << 4),
+        for (int c = 0; c < kCols / 8; ++c)
+          sts128(row + (uint32_t)(((c + kCols / 8 * cg) ^ (r & 7)) << 4),
                  make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]));
       }
       tc_fence_before();
@@ -1198,22 +1182,27 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       if (!last) continue;
 
       // ---- the piece's output ----
-      S.xl[tid] = l;
+      // (the buffer of the last block's neighbours: free again once all have met twice)
+      float* xl = S.xch[(g + 1) & 1];
+      xl[tid] = l;
       ok = meet();
       if (!ok) break;
-      const float lt = l + S.xl[tid ^ 64];
+      float lt = xl[r] + xl[r + 64];
+      if constexpr (kExp) lt += xl[r + 128] + xl[r + 192];
+      ok = meet();
+      if (!ok) break;
       ok = __all_sync(0xffffffffu, wait(&S.pv_done, g & 1));
       if (!ok) break;
       tc_fence_after();
-      const int f0 = hh * oc;                        // first feature of this thread
+      const int f0 = hh * oc + cg * ocg;             // first feature of this thread
       const int part = (cluster * 2 + dest) * 128 + (int)rank * 64 + r;
       // a sum of zero: no token seen (or none that exists)
       const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
       uint16_t* orow = static_cast<uint16_t*>(a.out) + (int64_t)row_q * a.o_st +
                        (int64_t)row_h * a.o_sh;
-      for (int c = 0; c < oc; c += 32) {
+      for (int c = 0; c < ocg; c += 32) {
         float o[32];
-        tmem_ld32(tmem + c + lanes, o);
+        tmem_ld32(obase + c, o);
         tmem_wait_ld();
         if (!row_ok) continue;
 #pragma unroll
@@ -1235,7 +1224,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
           }
         }
       }
-      if (hh == 0 && row_ok) {
+      if (hh == 0 && cg == 0 && row_ok) {
         if (dest >= 0) {
           P.w.ml[2 * (int64_t)part] = m;
           P.w.ml[2 * (int64_t)part + 1] = lt;
