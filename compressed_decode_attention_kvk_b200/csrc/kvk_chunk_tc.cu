@@ -146,6 +146,10 @@ __device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank) {
                    map_rank(smem_u32(bar), rank))
                : "memory");
 }
+template <typename T>
+__device__ __forceinline__ T uniform(T x) {
+  return __shfl_sync(0xffffffffu, x, 0);
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
@@ -207,25 +211,28 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
       : "memory");
 }
 
-// Bounded waits of one call: a wait that runs out stops both CTAs.
+// Bounded waits of one call: a wait that runs out stops both CTAs.  The loop is a function of its
+// own: inlined at every wait it pushes the roles' code out of the instruction cache.
+__device__ __noinline__ bool wait_slow(uint64_t* b, uint32_t parity, uint32_t abort_saddr,
+                                       uint64_t limit) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_hint(b, parity, 20000u)) {
+    if (abort_read(abort_saddr)) return false;
+    if (globaltimer() - t0 > limit) {
+      for (uint32_t r = 0; r < 2; ++r)
+        asm volatile("st.volatile.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(abort_saddr, r)),
+                     "r"(1u)
+                     : "memory");
+      return false;
+    }
+  }
+  return true;
+}
 struct Waiter {
   uint32_t abort_saddr;
   uint64_t limit;
   __device__ __forceinline__ bool operator()(uint64_t* b, uint32_t parity) const {
-    if (mbar_try(b, parity)) return true;
-    const uint64_t t0 = globaltimer();
-    while (!mbar_try_hint(b, parity, 20000u)) {
-      if (abort_read(abort_saddr)) return false;
-      if (globaltimer() - t0 > limit) {
-#pragma unroll
-        for (uint32_t r = 0; r < 2; ++r)
-          asm volatile("st.volatile.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(abort_saddr, r)),
-                       "r"(1u)
-                       : "memory");
-        return false;
-      }
-    }
-    return true;
+    return mbar_try(b, parity) || wait_slow(b, parity, abort_saddr, limit);
   }
 };
 
@@ -370,6 +377,10 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
   const ChunkArgs& a = P.a;
   Shared& S = *reinterpret_cast<Shared*>(smem + P.off_misc);
   const uint32_t q_s = smem_u32(smem), k_s = q_s + P.off_k, v_s = q_s + P.off_v, p_s = q_s + P.off_p;
+  // The warp index, and what a warp reads from shared memory to steer its MMAs, go through a
+  // shuffle: known to be the same in every lane, they and all that follows from them stay in
+  // uniform registers, where the MMA's operands have to be.  (A block's MMAs with their waits and
+  // commits: 2264 cycles issued so, 4545 from per-lane registers.)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cta_rank();
   const int cluster = blockIdx.x >> 1;
@@ -498,7 +509,88 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
   const Waiter wait{smem_u32(&S.abort_word), a.limit_ns};
   const int nch = (P.NV + 1) >> 1;       // output MMA steps over the features: 2 atoms, or the last 1
 
-  if (warp == kTokWarp) {
+  if (uniform(warp) == kMmaWarp) {
+    // ======================= MMA issuer =========================================================
+    if (rank == 0) {   // the whole warp, converged
+      auto all = [&](uint64_t* b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, wait(b, parity));
+      };
+      const uint64_t q0 = sdesc(q_s, 16u, 1024u, kLayoutSw128);
+      const uint64_t kb0 = sdesc(k_s, 16u, 1024u, kLayoutSw128);
+      const uint64_t p0 = sdesc(p_s, 16u, 1024u, kLayoutSw128);
+      const uint64_t vb0 = sdesc(v_s, kAtom, 1024u, kLayoutSw128);
+      const uint32_t tmem = uniform(S.tmem_base);
+      int kslot = 0;
+      uint32_t kpar = 0;
+      bool first_prev = false;
+      // output MMAs of block g (its first of a piece starts the sums anew)
+      auto output = [&](int g, bool first) -> bool {
+        if (!all(&S.p_ready, g & 1)) return false;
+        tc_fence_after();   // the softmax's reads of S and stores to O
+        const int vs = g % P.NVS;
+        const uint32_t vpar = (g / P.NVS) & 1;
+        for (int ch = 0; ch < nch; ++ch) {
+          if (!all(&S.v_ready[vs * 2 + ch], vpar)) return false;
+          const bool two = 2 * ch + 2 <= P.NV;
+          const uint32_t idesc = two ? P.idesc_o2 : P.idesc_o1;
+          const uint32_t hstep = (two ? 2 * kAtom : kAtom) >> 4;
+          const uint64_t vb = vb0 + ((uint32_t)(vs * 2 * P.NV + 4 * ch) * kAtom >> 4);
+          const uint32_t dcol = tmem + 128u * ch;
+          mma2x4(dcol, p0, vb, 128u, idesc, first ? 0u : 1u);
+          mma2x4(dcol, p0 + (kAtom >> 4), vb + hstep, 128u, idesc, 1u);
+          commit_both(&S.v_empty[vs * 2 + ch]);
+        }
+        commit_both(&S.pv_done);
+        return true;
+      };
+      bool ok = true;
+      int g = 0, pieces = 0;
+      for (;; ++g) {
+        const int st = g % kTokStages;
+        ok = all(&S.tok_full[st], (g / kTokStages) & 1);
+        if (!ok) break;
+        const int fl = uniform(*const_cast<volatile int32_t*>(&S.tok[st].flags));
+        if (lane == 0) mbar_arrive(&S.tok_empty[st]);
+        if (fl & kEnd) break;
+        if (fl & kFirst) {
+          ok = all(&S.q_ready, pieces & 1);
+          if (!ok) break;
+        }
+        const uint32_t scol = tmem + kSCol + 64u * (g & 1);
+        const int parts = kLo ? 2 : 1;
+        for (int at = 0; ok && at < P.NA; ++at) {
+          for (int part = 0; part < parts; ++part) {
+            ok = all(&S.k_ready[kslot], kpar);
+            if (!ok) break;
+            const uint64_t ad = q0 + ((uint32_t)at * kAtom >> 4);
+            const uint64_t bd = kb0 + ((uint32_t)kslot * kAtom >> 4);
+            mma2x4(scol, ad, bd, 2u, P.idesc_s, (at > 0 || part > 0) ? 1u : 0u);
+            commit_both(&S.k_empty[kslot]);
+            if (++kslot == P.NK) {
+              kslot = 0;
+              kpar ^= 1;
+            }
+          }
+        }
+        if (!ok) break;
+        commit_both(&S.s_full[g & 1]);
+        if (fl & kLast) {
+          commit_both(&S.q_empty);
+          ++pieces;
+        }
+        if (g > 0) {
+          ok = output(g - 1, first_prev);
+          if (!ok) break;
+        }
+        first_prev = (fl & kFirst) != 0;
+      }
+      if (ok && g > 0) ok = output(g - 1, first_prev);
+      // every MMA and its arrivals are done before either CTA leaves
+      __syncwarp();
+      commit_both(&S.drain);
+      drain(&S.drain, 0u);
+    }
+  } else if (warp == kTokWarp) {
     // ======================= token warp: pieces, slots, scales ==================================
     int seq = S.start_seq, k = S.start_k;
     int64_t base = S.start_base;
@@ -604,87 +696,6 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         S.tok[st].flags = kEnd;
         mbar_arrive(&S.tok_full[st]);
       }
-    }
-  } else if (warp == kMmaWarp) {
-    // ======================= MMA issuer =========================================================
-    if (rank == 0) {   // the whole warp, converged
-      auto all = [&](uint64_t* b, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, wait(b, parity));
-      };
-      const uint64_t q0 = sdesc(q_s, 16u, 1024u, kLayoutSw128);
-      const uint64_t kb0 = sdesc(k_s, 16u, 1024u, kLayoutSw128);
-      const uint64_t p0 = sdesc(p_s, 16u, 1024u, kLayoutSw128);
-      const uint64_t vb0 = sdesc(v_s, kAtom, 1024u, kLayoutSw128);
-      int kslot = 0;
-      uint32_t kpar = 0;
-      bool first_prev = false;
-      // output MMAs of block g (its first of a piece starts the sums anew)
-      auto output = [&](int g, bool first) -> bool {
-        if (!all(&S.p_ready, g & 1)) return false;
-        tc_fence_after();   // the softmax's reads of S and stores to O
-        const int vs = g % P.NVS;
-        const uint32_t vpar = (g / P.NVS) & 1;
-        for (int ch = 0; ch < nch; ++ch) {
-          if (!all(&S.v_ready[vs * 2 + ch], vpar)) return false;
-          const bool two = 2 * ch + 2 <= P.NV;
-          const uint32_t idesc = two ? P.idesc_o2 : P.idesc_o1;
-          const uint32_t hstep = (two ? 2 * kAtom : kAtom) >> 4;
-          const uint64_t vb = vb0 + ((uint32_t)(vs * 2 * P.NV + 4 * ch) * kAtom >> 4);
-          const uint32_t dcol = tmem + 128u * ch;
-          mma2x4(dcol, p0, vb, 128u, idesc, first ? 0u : 1u);
-          mma2x4(dcol, p0 + (kAtom >> 4), vb + hstep, 128u, idesc, 1u);
-          commit_both(&S.v_empty[vs * 2 + ch]);
-        }
-        commit_both(&S.pv_done);
-        return true;
-      };
-      bool ok = true;
-      int g = 0, pieces = 0;
-      for (;; ++g) {
-        const int st = g % kTokStages;
-        ok = all(&S.tok_full[st], (g / kTokStages) & 1);
-        if (!ok) break;
-        const int fl = *const_cast<volatile int32_t*>(&S.tok[st].flags);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.tok_empty[st]);
-        if (fl & kEnd) break;
-        if (fl & kFirst) {
-          ok = all(&S.q_ready, pieces & 1);
-          if (!ok) break;
-        }
-        const uint32_t scol = tmem + kSCol + 64u * (g & 1);
-        const int parts = kLo ? 2 : 1;
-        for (int at = 0; ok && at < P.NA; ++at) {
-          for (int part = 0; part < parts; ++part) {
-            ok = all(&S.k_ready[kslot], kpar);
-            if (!ok) break;
-            const uint64_t ad = q0 + ((uint32_t)at * kAtom >> 4);
-            const uint64_t bd = kb0 + ((uint32_t)kslot * kAtom >> 4);
-            mma2x4(scol, ad, bd, 2u, P.idesc_s, (at > 0 || part > 0) ? 1u : 0u);
-            commit_both(&S.k_empty[kslot]);
-            if (++kslot == P.NK) {
-              kslot = 0;
-              kpar ^= 1;
-            }
-          }
-        }
-        if (!ok) break;
-        commit_both(&S.s_full[g & 1]);
-        if (fl & kLast) {
-          commit_both(&S.q_empty);
-          ++pieces;
-        }
-        if (g > 0) {
-          ok = output(g - 1, first_prev);
-          if (!ok) break;
-        }
-        first_prev = (fl & kFirst) != 0;
-      }
-      if (ok && g > 0) ok = output(g - 1, first_prev);
-      // every MMA and its arrivals are done before either CTA leaves
-      __syncwarp();
-      commit_both(&S.drain);
-      drain(&S.drain, 0u);
     }
   } else if (warp == kRelayWarp) {
     // ======================= relay ==============================================================
