@@ -167,19 +167,26 @@ __device__ __forceinline__ void commit_both(uint64_t* bar) {
 // Four MMAs of the pair, D (+)= A_k B_k, issued by the elected lane of a converged warp: with the
 // descriptors in uniform registers the pattern of one block (36 score and 16 output MMAs) takes
 // 2380 cycles with its commits (2176 at the full rate); a lone thread issuing them took 6500.
-__device__ __forceinline__ void mma2x4(uint32_t d, uint64_t a, uint64_t b, uint32_t b_step,
-                                       uint32_t idesc, uint32_t acc) {
-  const uint64_t a1 = a + 2, a2 = a + 4, a3 = a + 6;      // K steps of 16: 32 bytes
-  const uint64_t b1 = b + b_step, b2 = b + 2u * b_step, b3 = b + 3u * b_step;
+// a, b: low words of the descriptors, hi: their common high word.
+__device__ __forceinline__ void mma2x4(uint32_t d, uint32_t a, uint32_t b, uint32_t b_step,
+                                       uint32_t hi_a, uint32_t hi_b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 x0, x1, x2, x3, y0, y1, y2, y3;\n\t.reg .b32 t;\n\t"
+      "mov.b64 x0, {%1, %4};\n\t"
+      "add.u32 t, %1, 2;\n\tmov.b64 x1, {t, %4};\n\t"     // K steps of 16: 32 bytes
+      "add.u32 t, %1, 4;\n\tmov.b64 x2, {t, %4};\n\t"
+      "add.u32 t, %1, 6;\n\tmov.b64 x3, {t, %4};\n\t"
+      "mov.b64 y0, {%2, %5};\n\t"
+      "add.u32 t, %2, %3;\n\tmov.b64 y1, {t, %5};\n\t"
+      "add.u32 t, t, %3;\n\tmov.b64 y2, {t, %5};\n\t"
+      "add.u32 t, t, %3;\n\tmov.b64 y3, {t, %5};\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %10, 0;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %5, %9, p;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %2, %6, %9, 1;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %3, %7, %9, 1;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %4, %8, %9, 1;\n\t}" ::"r"(d),
-      "l"(a), "l"(a1), "l"(a2), "l"(a3), "l"(b), "l"(b1), "l"(b2), "l"(b3), "r"(idesc), "r"(acc)
+      "setp.ne.b32 p, %7, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], x0, y0, %6, p;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], x1, y1, %6, 1;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], x2, y2, %6, 1;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], x3, y3, %6, 1;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(b_step), "r"(hi_a), "r"(hi_b), "r"(idesc), "r"(acc)
       : "memory");
 }
 // 32 lanes x 32 columns: thread i of the warp holds lane base + i
@@ -264,7 +271,7 @@ __device__ __forceinline__ int blocks_of(int len, int count, int H, int flat0, i
 // operands is scaled by the power of two that brings its row's largest element into
 // [2^14, 2^15); other queries are copied.  A negative softmax scale flips the sign.
 template <bool OP_BF16>
-__device__ __forceinline__ void stage_query(const TcChunk& P, Shared& S, uint32_t q_saddr,
+__device__ __noinline__ void stage_query(const TcChunk& P, Shared& S, uint32_t q_saddr,
                                             const QueryTile& h, int rank, int r0, int r1) {
   const int lane = threadIdx.x & 31;
   const int chunks = P.NA * 8;                    // 16-byte chunks of 8 features
@@ -274,6 +281,7 @@ __device__ __forceinline__ void stage_query(const TcChunk& P, Shared& S, uint32_
   constexpr int kR = 2;
   const uint16_t* qlat = static_cast<const uint16_t*>(P.a.q_lat);
   const uint16_t* qrope = static_cast<const uint16_t*>(P.a.q_rope);
+#pragma unroll 1
   for (int r = r0; r < r1; r += kR) {
     uint4 v[kR][kC];
 #pragma unroll
@@ -439,6 +447,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     const int i0 = min(a.batch, tid * per), i1 = min(a.batch, i0 + per);
     int64_t tiles = 0, total_tiles = 0, total = 0;
     bool bad_rows = false, bad_len = false;
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) {
       const int s0 = __ldg(a.q_start + i), s1 = __ldg(a.q_start + i + 1), l = __ldg(a.seq_lens + i);
       bad_rows = bad_rows || s0 < 0 || s1 < s0 || s1 > a.n_q;
@@ -449,6 +458,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     if ((bad_rows || bad_len) && blockIdx.x == 0) atomicOr(a.flags, KVK_FLAG_SEQ_LEN);
     int64_t at = block_scan(stop ? 0 : tiles, S.scan, &total_tiles);
     if (!stop) {
+#pragma unroll 1
       for (int i = i0; i < i1; ++i) {
         const int s0 = __ldg(a.q_start + i), s1 = __ldg(a.q_start + i + 1);
         pre[i] = (int32_t)at;
@@ -471,9 +481,11 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       seq0 = lo;
     }
     int64_t cost = 0, base = 0;
+#pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
       int seq = seq0, loaded = -1;
       ChunkSeq s = {0, 0, 0};
+#pragma unroll 1
       for (int f = f0; f < f1; ++f) {
         while (pre[seq + 1] <= f) ++seq;
         if (loaded != seq) {
@@ -516,75 +528,72 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         return __all_sync(0xffffffffu, wait(b, parity));
       };
       const uint64_t q0 = sdesc(q_s, 16u, 1024u, kLayoutSw128);
-      const uint64_t kb0 = sdesc(k_s, 16u, 1024u, kLayoutSw128);
-      const uint64_t p0 = sdesc(p_s, 16u, 1024u, kLayoutSw128);
       const uint64_t vb0 = sdesc(v_s, kAtom, 1024u, kLayoutSw128);
+      const uint32_t hk = (uint32_t)(q0 >> 32), hv = (uint32_t)(vb0 >> 32);
+      const uint32_t ql = (uint32_t)q0, vl = (uint32_t)vb0;
+      const uint32_t kl = ql + (P.off_k >> 4), pl = ql + (P.off_p >> 4);
+      constexpr uint32_t kA = kAtom >> 4;             // an atom in descriptor units
       const uint32_t tmem = uniform(S.tmem_base);
-      int kslot = 0;
+      int kslot = 0, pieces = 0;
       uint32_t kpar = 0;
-      bool first_prev = false;
-      // output MMAs of block g (its first of a piece starts the sums anew)
-      auto output = [&](int g, bool first) -> bool {
-        if (!all(&S.p_ready, g & 1)) return false;
-        tc_fence_after();   // the softmax's reads of S and stores to O
-        const int vs = g % P.NVS;
-        const uint32_t vpar = (g / P.NVS) & 1;
-        for (int ch = 0; ch < nch; ++ch) {
-          if (!all(&S.v_ready[vs * 2 + ch], vpar)) return false;
-          const bool two = 2 * ch + 2 <= P.NV;
-          const uint32_t idesc = two ? P.idesc_o2 : P.idesc_o1;
-          const uint32_t hstep = (two ? 2 * kAtom : kAtom) >> 4;
-          const uint64_t vb = vb0 + ((uint32_t)(vs * 2 * P.NV + 4 * ch) * kAtom >> 4);
-          const uint32_t dcol = tmem + 128u * ch;
-          mma2x4(dcol, p0, vb, 128u, idesc, first ? 0u : 1u);
-          mma2x4(dcol, p0 + (kAtom >> 4), vb + hstep, 128u, idesc, 1u);
-          commit_both(&S.v_empty[vs * 2 + ch]);
-        }
-        commit_both(&S.pv_done);
-        return true;
-      };
+      int fl = 0;                                     // flags of the block before
       bool ok = true;
-      int g = 0, pieces = 0;
-      for (;; ++g) {
+      // block g: its score MMAs, then the output MMAs of block g - 1, whose softmax they cover
+      for (int g = 0;; ++g) {
         const int st = g % kTokStages;
         ok = all(&S.tok_full[st], (g / kTokStages) & 1);
         if (!ok) break;
-        const int fl = uniform(*const_cast<volatile int32_t*>(&S.tok[st].flags));
+        const int now = uniform(*const_cast<volatile int32_t*>(&S.tok[st].flags));
         if (lane == 0) mbar_arrive(&S.tok_empty[st]);
-        if (fl & kEnd) break;
-        if (fl & kFirst) {
-          ok = all(&S.q_ready, pieces & 1);
-          if (!ok) break;
-        }
-        const uint32_t scol = tmem + kSCol + 64u * (g & 1);
-        const int parts = kLo ? 2 : 1;
-        for (int at = 0; ok && at < P.NA; ++at) {
-          for (int part = 0; part < parts; ++part) {
+        if (!(now & kEnd)) {
+          if (now & kFirst) ok = all(&S.q_ready, pieces & 1);
+          const uint32_t scol = tmem + kSCol + 64u * (g & 1);
+          uint32_t acc = 0, qa = ql;
+#pragma unroll 1
+          for (int i = 0; ok && i < P.NA * (kLo ? 2 : 1); ++i) {
             ok = all(&S.k_ready[kslot], kpar);
             if (!ok) break;
-            const uint64_t ad = q0 + ((uint32_t)at * kAtom >> 4);
-            const uint64_t bd = kb0 + ((uint32_t)kslot * kAtom >> 4);
-            mma2x4(scol, ad, bd, 2u, P.idesc_s, (at > 0 || part > 0) ? 1u : 0u);
+            mma2x4(scol, qa, kl + (uint32_t)kslot * kA, 2u, hk, hk, P.idesc_s, acc);
             commit_both(&S.k_empty[kslot]);
+            acc = 1;
+            if (!kLo || (i & 1)) qa += kA;
             if (++kslot == P.NK) {
               kslot = 0;
               kpar ^= 1;
             }
           }
-        }
-        if (!ok) break;
-        commit_both(&S.s_full[g & 1]);
-        if (fl & kLast) {
-          commit_both(&S.q_empty);
-          ++pieces;
+          if (!ok) break;
+          commit_both(&S.s_full[g & 1]);
+          if (now & kLast) {
+            commit_both(&S.q_empty);
+            ++pieces;
+          }
         }
         if (g > 0) {
-          ok = output(g - 1, first_prev);
+          // (the first block of a piece starts the sums anew)
+          ok = all(&S.p_ready, (g - 1) & 1);
           if (!ok) break;
+          tc_fence_after();   // the softmax's reads of S and stores to O
+          const int vs = (g - 1) % P.NVS;
+          const uint32_t vpar = ((g - 1) / P.NVS) & 1;
+          const uint32_t acc = (fl & kFirst) ? 0u : 1u;
+          uint32_t vb = vl + (uint32_t)(vs * 2 * P.NV) * kA;
+#pragma unroll 1
+          for (int ch = 0; ch < nch; ++ch, vb += 4 * kA) {
+            ok = all(&S.v_ready[vs * 2 + ch], vpar);
+            if (!ok) break;
+            const bool two = 2 * ch + 2 <= P.NV;
+            const uint32_t idesc = two ? P.idesc_o2 : P.idesc_o1;
+            mma2x4(tmem + 128u * ch, pl, vb, 128u, hk, hv, idesc, acc);
+            mma2x4(tmem + 128u * ch, pl + kA, vb + (two ? 2 * kA : kA), 128u, hk, hv, idesc, 1u);
+            commit_both(&S.v_empty[vs * 2 + ch]);
+          }
+          if (!ok) break;
+          commit_both(&S.pv_done);
         }
-        first_prev = (fl & kFirst) != 0;
+        if (now & kEnd) break;
+        fl = now;
       }
-      if (ok && g > 0) ok = output(g - 1, first_prev);
       // every MMA and its arrivals are done before either CTA leaves
       __syncwarp();
       commit_both(&S.drain);
@@ -605,6 +614,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         const int64_t x0 = u0 - base - kPieceCost, x1 = u1 - base - kPieceCost;
         const int b0 = (int)max((int64_t)0, min(x0, (int64_t)nblk));
         const int b1 = (int)max((int64_t)0, min(x1, (int64_t)nblk));
+#pragma unroll 1
         for (int blk = b0; ok && blk < b1; ++blk, ++g) {
           const int st = g % kTokStages;
           ok = wait(&S.tok_empty[st], ((g / kTokStages) & 1) ^ 1);
@@ -710,37 +720,37 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         arrive_at(ready, 0);
         return true;
       };
-      auto output = [&](int g) -> bool {
-        if (!pass(&S.p_full, &S.p_ready, g & 1)) return false;
-        for (int ch = 0; ch < nch; ++ch) {
-          const int v = g % P.NVS * 2 + ch;
-          if (!pass(&S.v_full[v], &S.v_ready[v], (g / P.NVS) & 1)) return false;
-        }
-        return true;
-      };
-      int kslot = 0, pieces = 0, g = 0;
+      int kslot = 0, pieces = 0;
       uint32_t kpar = 0;
       bool ok = true;
-      for (;; ++g) {
+      for (int g = 0; ok; ++g) {
         const int st = g % kTokStages;
         ok = wait(&S.tok_full[st], (g / kTokStages) & 1);
         if (!ok) break;
         const int fl = *const_cast<volatile int32_t*>(&S.tok[st].flags);
         mbar_arrive(&S.tok_empty[st]);
-        if (fl & kEnd) break;
-        if (fl & kFirst) ok = pass(&S.q_full, &S.q_ready, pieces & 1);
-        if (fl & kLast) ++pieces;
-        for (int i = 0; ok && i < P.NA * (kLo ? 2 : 1); ++i) {
-          ok = pass(&S.k_full[kslot], &S.k_ready[kslot], kpar);
-          if (++kslot == P.NK) {
-            kslot = 0;
-            kpar ^= 1;
+        if (!(fl & kEnd)) {
+          if (fl & kFirst) ok = pass(&S.q_full, &S.q_ready, pieces & 1);
+          if (fl & kLast) ++pieces;
+#pragma unroll 1
+          for (int i = 0; ok && i < P.NA * (kLo ? 2 : 1); ++i) {
+            ok = pass(&S.k_full[kslot], &S.k_ready[kslot], kpar);
+            if (++kslot == P.NK) {
+              kslot = 0;
+              kpar ^= 1;
+            }
           }
         }
-        if (ok && g > 0) ok = output(g - 1);
-        if (!ok) break;
+        if (ok && g > 0) {
+          ok = pass(&S.p_full, &S.p_ready, (g - 1) & 1);
+          const int vs = (g - 1) % P.NVS * 2;
+          const uint32_t vpar = ((g - 1) / P.NVS) & 1;
+#pragma unroll 1
+          for (int ch = 0; ok && ch < nch; ++ch)
+            ok = pass(&S.v_full[vs + ch], &S.v_ready[vs + ch], vpar);
+        }
+        if (fl & kEnd) break;
       }
-      if (ok && g > 0) output(g - 1);
     }
   } else if (warp == kLoadWarp) {
     // ======================= K loads (expanded rows) ============================================
@@ -759,6 +769,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.tok_empty[st]);
+#pragma unroll 1
       for (int i = 0; i < P.NA * (kLo ? 2 : 1); ++i) {
         const int at = kLo ? i >> 1 : i;
         ok = __all_sync(0xffffffffu, wait(&S.k_empty[kslot], kpar));
@@ -776,6 +787,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     }
     // loads in flight land before the CTA's memory goes (only a stopped kernel has any)
     if (kExp && lane == 0)
+#pragma unroll 1
       for (int j = 0; j < P.NK; ++j) drain(&S.k_full[j], j < kslot ? kpar ^ 1 : kpar);
   } else if (kExp && warp >= kVWarp0) {
     // ======================= V loads (expanded rows) ============================================
@@ -807,6 +819,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       const uint32_t vpar = (g / P.NVS) & 1;
       const uint32_t stage = P.off_v + (uint32_t)(vs * 2 * P.NV) * kAtom;
       if (vw == 0) {
+#pragma unroll 1
         for (int ch = 0; ok && ch < nch; ++ch) {
           const int nj = min(2, P.NV - 2 * ch);
           ok = __all_sync(0xffffffffu, wait(&S.v_empty[vs * 2 + ch], vpar ^ 1));
@@ -817,6 +830,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
           __syncwarp();
           // one box a lane: token row group, atom of the step
           const int per = 128 / P.box;
+#pragma unroll 1
           for (int i = lane; i < per * nj; i += 32) {
             const int jj = i / per, t = (i - jj * per) * P.box;
             const int sl = T.slot[t];
@@ -832,11 +846,13 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       const int live = min(128, T.len - T.t0);       // rows that hold tokens
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.tok_empty[st]);
+#pragma unroll 1
       for (int ch = 0; ch < nch; ++ch) {
         const int nj = min(2, P.NV - 2 * ch);
         ok = __all_sync(0xffffffffu, wait(&S.v_land[vs * 2 + ch], vpar));
         if (!ok) break;
         if (live < 128) {                             // 8 lanes a row
+#pragma unroll 1
           for (int t = max(live, 0) + (vt >> 3); t < 128; t += 16)
             for (int jj = 0; jj < nj; ++jj)
               sts128(q_s + stage + (uint32_t)(4 * ch + (t >> 6) * nj + jj) * kAtom +
@@ -890,6 +906,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       const int vs = g % P.NVS;
       const uint32_t vpar = ((g / P.NVS) & 1) ^ 1;
       const uint32_t stage = v_s + (uint32_t)(vs * 2 * P.NV) * kAtom;
+#pragma unroll 1
       for (int j0 = 0; j0 < P.NV; j0 += 2) {
         const int ch = j0 >> 1;
         const bool two = j0 + 2 <= P.NV;
@@ -1170,6 +1187,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         tc_fence_after();
       }
       if (!(fl & kFirst) && __any_sync(0xffffffffu, alpha != 1.0f)) {
+#pragma unroll 1
         for (int c = 0; c < ocg; c += 32) {
           float o[32];
           tmem_ld32(obase + c, o);
@@ -1211,6 +1229,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
       uint16_t* orow = static_cast<uint16_t*>(a.out) + (int64_t)row_q * a.o_st +
                        (int64_t)row_h * a.o_sh;
+#pragma unroll 1
       for (int c = 0; c < ocg; c += 32) {
         float o[32];
         tmem_ld32(obase + c, o);
