@@ -79,9 +79,31 @@ chunk_expand_kernel(const __grid_constant__ ChunkArgs a, uint8_t* __restrict__ h
   }
 }
 
+// The rows between a sequence's end and the end of the last box that it reads hold anything, NaN
+// among it, which a zero weight does not silence: they become zero, ahead of the conversion (the
+// page may be shared with a longer sequence, whose rows are written after it).
+__global__ void __launch_bounds__(256)
+chunk_tail_kernel(const __grid_constant__ ChunkArgs a, uint8_t* __restrict__ hi_p,
+                  uint8_t* __restrict__ lo_p, int NA, int box) {
+  bool bad;
+  const ChunkSeq s = chunk_seq(a, blockIdx.x, &bad);
+  const int rest = -s.len & (box - 1);
+  if (s.count == 0 || rest == 0) return;
+  const int slot = chunk_slot(a, blockIdx.x, s.len - 1);
+  if (slot < 0) return;
+  const int64_t from = (int64_t)(slot + 1) * NA * 8;      // 16-byte words
+  for (int i = threadIdx.x; i < rest * NA * 8; i += blockDim.x) {
+    reinterpret_cast<uint4*>(hi_p)[from + i] = make_uint4(0u, 0u, 0u, 0u);
+    if (lo_p) reinterpret_cast<uint4*>(lo_p)[from + i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
 template <int BITS, bool GROUP>
 cudaError_t launch(const ChunkArgs& a, const ChunkWork& w, cudaStream_t st) {
   // about four CTAs per SM over the whole batch, each at least one round of a sequence
+  const int box = std::min(1 << a.page_shift, 64);
+  chunk_tail_kernel<<<dim3(a.batch), dim3(256), 0, st>>>(
+      a, static_cast<uint8_t*>(w.hi), static_cast<uint8_t*>(w.lo), row_atoms(a.d, a.d_rope), box);
   const int per_round = kExpandWarps * kTokens;
   const int rounds = (a.cap + per_round - 1) / per_round;
   const int gx = std::max(1, std::min(rounds, (8 * 2 * w.G + a.batch - 1) / a.batch));

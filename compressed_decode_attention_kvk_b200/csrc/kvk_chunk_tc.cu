@@ -28,6 +28,12 @@
 //   14     relay: passes the barriers of written operands on to the leader
 // Both teams stage the query rows at a piece's start.
 //
+// With expanded rows (kvk_chunk_expand.cu) nothing is converted here: warps 4-7 are a second set of
+// softmax warps (32 tokens a thread), warp 15 loads K, two atoms a ring slot, warp 8 V (TMA, counted
+// on the leader's barriers), warps 8-11 stage the query, and there is no relay.  What a block costs
+// beside its MMAs is the hand-over at the barriers (a skeleton without MMAs, loads and softmax took
+// 4200 cycles a block with a relay and single atoms), hence few and large steps.
+//
 // Numbers.  Codes enter the MMA exactly: a code of at most 8 bits is an f16 integer; a 16-bit
 // code c and a group-scaled value c s are split into two f16 parts (hi = f16(x), lo = x - hi)
 // whose score MMAs add up.  The output MMA takes the high part (relative 2^-12) and P in f16
@@ -90,7 +96,7 @@ struct Shared {
   uint64_t tok_full[kTokStages], tok_empty[kTokStages];
   // operands: written (by this CTA's warps), passed on (to the leader, by both relays), free
   uint64_t k_full[kMaxK], k_ready[kMaxK], k_empty[kMaxK];
-  uint64_t v_land[4], v_full[4], v_ready[4], v_empty[4];
+  uint64_t v_full[4], v_ready[4], v_empty[4];
   uint64_t q_full, q_ready, q_empty, q_local[4];
   uint64_t s_full[2], p_full, p_ready, pv_done, x_bar, drain;
   int64_t scan[kWarps + 1];
@@ -215,6 +221,17 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
       "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]),
       "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]),
       "f"(v[29]), "f"(v[30]), "f"(v[31])
+      : "memory");
+}
+
+// Loads a box into this CTA's shared memory, counted on the barrier at cluster address `bar` (the
+// leader's: the MMA that reads the pair's operands waits for both CTAs' loads there).
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* tmap, int x, int y,
+                                              uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
 
@@ -381,6 +398,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
   constexpr bool kTok = !GROUP && !kBf16;             // one scale per token
   constexpr bool kLo = kSplit<BITS, GROUP>;
   constexpr int kSoftWarps = kExp ? 8 : 4;
+  constexpr int kStep = kExp ? 2 : 1;                 // atoms of a K ring slot
   extern __shared__ __align__(1024) uint8_t smem[];
   const ChunkArgs& a = P.a;
   Shared& S = *reinterpret_cast<Shared*>(smem + P.off_misc);
@@ -398,28 +416,27 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     S.abort_word = 0;
     for (int i = 0; i < kTokStages; ++i) {
       mbar_init(&S.tok_full[i], 1);
-      // softmax warps, converting or loading warps, relay, the leader's MMA warp
-      mbar_init(&S.tok_empty[i], kSoftWarps + (kExp ? 5 : 8) + 1 + (rank == 0 ? 1 : 0));
+      // softmax warps, loading or converting warps and relay, the leader's MMA warp
+      mbar_init(&S.tok_empty[i], kSoftWarps + (kExp ? 5 : 9) + (rank == 0 ? 1 : 0));
     }
     for (int i = 0; i < kMaxK; ++i) {
-      mbar_init(&S.k_full[i], kExp ? 1 : 4);
-      mbar_init(&S.k_ready[i], 2);
+      mbar_init(&S.k_full[i], 4);
+      mbar_init(&S.k_ready[i], kExp ? 1 : 2);      // loads: one arming for both CTAs' bytes
       mbar_init(&S.k_empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&S.v_land[i], 1);
       mbar_init(&S.v_full[i], 4);
-      mbar_init(&S.v_ready[i], 2);
+      mbar_init(&S.v_ready[i], kExp ? 1 : 2);
       mbar_init(&S.v_empty[i], 1);
       mbar_init(&S.q_local[i], kExp ? 4 : 8);
     }
-    mbar_init(&S.q_full, kExp ? 4 : 8);
-    mbar_init(&S.q_ready, 2);
+    mbar_init(&S.q_full, 8);
+    mbar_init(&S.q_ready, kExp ? 8 : 2);
     mbar_init(&S.q_empty, 1);
     mbar_init(&S.s_full[0], 1);
     mbar_init(&S.s_full[1], 1);
     mbar_init(&S.p_full, kSoftWarps);
-    mbar_init(&S.p_ready, 2);
+    mbar_init(&S.p_ready, kExp ? 2 * kSoftWarps : 2);
     mbar_init(&S.pv_done, 1);
     mbar_init(&S.x_bar, kSoftWarps);
     mbar_init(&S.drain, 1);
@@ -547,16 +564,23 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         if (lane == 0) mbar_arrive(&S.tok_empty[st]);
         if (!(now & kEnd)) {
           if (now & kFirst) ok = all(&S.q_ready, pieces & 1);
+          if (!ok) break;
           const uint32_t scol = tmem + kSCol + 64u * (g & 1);
           uint32_t acc = 0, qa = ql;
+          const int atoms = P.NA * (kLo ? 2 : 1);
 #pragma unroll 1
-          for (int i = 0; ok && i < P.NA * (kLo ? 2 : 1); ++i) {
+          for (int i = 0; i < atoms; i += kStep) {
             ok = all(&S.k_ready[kslot], kpar);
             if (!ok) break;
-            mma2x4(scol, qa, kl + (uint32_t)kslot * kA, 2u, hk, hk, P.idesc_s, acc);
+            const uint32_t kb = kl + (uint32_t)(kslot * kStep) * kA;
+            mma2x4(scol, qa, kb, 2u, hk, hk, P.idesc_s, acc);
+            if (!kLo || (kStep == 1 && (i & 1))) qa += kA;
+            if (kStep == 2) {        // the next atom, or the low part of the same elements
+              if (i + 1 < atoms) mma2x4(scol, qa, kb + kA, 2u, hk, hk, P.idesc_s, 1u);
+              qa += kA;
+            }
             commit_both(&S.k_empty[kslot]);
             acc = 1;
-            if (!kLo || (i & 1)) qa += kA;
             if (++kslot == P.NK) {
               kslot = 0;
               kpar ^= 1;
@@ -713,7 +737,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     // makes the proxy fence for the threads that wrote the operands, whose own would wait for
     // all their loads in flight (measured 1600 cycles per atom of the K team), and the MMA
     // issuer's for its MMAs.
-    if (lane == 0) {
+    if (!kExp && lane == 0) {
       auto pass = [&](uint64_t* b, uint64_t* ready, uint32_t parity) -> bool {
         if (!wait(b, parity)) return false;
         fence_proxy_async_smem();
@@ -761,39 +785,40 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       const int st = g % kTokStages;
       ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], (g / kTokStages) & 1));
       if (!ok || (S.tok[st].flags & kEnd)) break;
-      const int per = 64 / P.box;
-      int sl = P.pool_slots;
-      if (lane < per) {
-        const int x = S.tok[st].slot[64 * (int)rank + lane * P.box];
+      // a lane per box: slots of the block's boxes, atoms of the step
+      const int per = 64 / P.box, lg = 31 - __clz(per);
+      int sl = P.pool_slots;                          // reads as zero
+      if (lane < 2 * per) {
+        const int x = S.tok[st].slot[64 * (int)rank + (lane & (per - 1)) * P.box];
         if (x >= 0) sl = x;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.tok_empty[st]);
+      const int atoms = P.NA * (kLo ? 2 : 1), j = lane >> lg;
+      const uint32_t to = q_s + P.off_k + (uint32_t)j * kAtom + (uint32_t)((lane & (per - 1)) * P.box) * 128u;
+      const void* map = kLo && j ? &map_lo : &map_hi;
 #pragma unroll 1
-      for (int i = 0; i < P.NA * (kLo ? 2 : 1); ++i) {
-        const int at = kLo ? i >> 1 : i;
+      for (int i = 0; i < atoms; i += kStep) {
         ok = __all_sync(0xffffffffu, wait(&S.k_empty[kslot], kpar));
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&S.k_full[kslot], kAtom);
+        const int n = min(kStep, atoms - i);
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&S.k_ready[kslot], 2u * n * kAtom);
+        if (j < n)
+          tma_load_pair(to + (uint32_t)(kslot * kStep) * kAtom, map, (kLo ? i >> 1 : i + j) * 64, sl,
+                        map_rank(smem_u32(&S.k_ready[kslot]), 0));
         __syncwarp();
-        if (lane < per)
-          tma_load_2d(smem + P.off_k + (uint32_t)kslot * kAtom + (uint32_t)(lane * P.box) * 128u,
-                      (kLo && (i & 1)) ? &map_lo : &map_hi, at * 64, sl, &S.k_full[kslot]);
         if (++kslot == P.NK) {
           kslot = 0;
           kpar ^= 1;
         }
       }
     }
-    // loads in flight land before the CTA's memory goes (only a stopped kernel has any)
-    if (kExp && lane == 0)
-#pragma unroll 1
-      for (int j = 0; j < P.NK; ++j) drain(&S.k_full[j], j < kslot ? kpar ^ 1 : kpar);
+    // loads in flight (only a stopped kernel has any) land before either CTA's memory goes
+    if (kExp && rank == 0 && lane == 0)
+      for (int j = 0; j < P.NK; ++j) drain(&S.k_ready[j], j < kslot ? kpar ^ 1 : kpar);
   } else if (kExp && warp >= kVWarp0) {
-    // ======================= V loads (expanded rows) ============================================
-    // One thread loads the atoms; behind the last token the boxes hold whatever the rows there
-    // hold, so the team zeroes those rows before it passes the operand on.
-    const int vt = tid - kVWarp0 * 32, vw = warp - kVWarp0;
+    // ======================= V loads (expanded rows), query rows ================================
+    const int vw = warp - kVWarp0;
     uint32_t armed = 0, landing = 0;                  // barriers used so far, and their last phase
     bool ok = true;
     for (int g = 0;; ++g) {
@@ -809,64 +834,47 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         stage_query<kBf16>(P, S, q_s, head, (int)rank, vw * 16, vw * 16 + 16);
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&S.q_local[head.piece & 3]);
-          mbar_arrive(&S.q_full);
+          arrive_at(&S.q_ready, 0);
         }
       }
-      const int vs = g % P.NVS;
-      const uint32_t vpar = (g / P.NVS) & 1;
-      const uint32_t stage = P.off_v + (uint32_t)(vs * 2 * P.NV) * kAtom;
       if (vw == 0) {
+        const int vs = g % P.NVS;
+        const uint32_t vpar = (g / P.NVS) & 1;
+        const uint32_t stage = q_s + P.off_v + (uint32_t)(vs * 2 * P.NV) * kAtom;
+        // a lane per box: slots of the block's boxes, atoms of the step
+        const int per = 128 / P.box;
 #pragma unroll 1
-        for (int ch = 0; ok && ch < nch; ++ch) {
+        for (int ch = 0; ch < nch; ++ch) {
           const int nj = min(2, P.NV - 2 * ch);
+          uint64_t* bar = &S.v_ready[vs * 2 + ch];
           ok = __all_sync(0xffffffffu, wait(&S.v_empty[vs * 2 + ch], vpar ^ 1));
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&S.v_land[vs * 2 + ch], 2u * nj * kAtom);
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar, 2u * 2u * nj * kAtom);
           armed |= 1u << (vs * 2 + ch);
           landing = (landing & ~(1u << (vs * 2 + ch))) | vpar << (vs * 2 + ch);
-          __syncwarp();
-          // one box a lane: token row group, atom of the step
-          const int per = 128 / P.box;
 #pragma unroll 1
           for (int i = lane; i < per * nj; i += 32) {
-            const int jj = i / per, t = (i - jj * per) * P.box;
+            const int jj = i >= per, t = (i - jj * per) * P.box;
             const int sl = T.slot[t];
-            const uint32_t at = stage + (uint32_t)(4 * ch + (t >> 6) * nj + jj) * kAtom +
-                                (uint32_t)(t & 63) * 128u;
-            tma_load_2d(smem + at, &map_hi, ((int)rank * P.NV + 2 * ch + jj) * 64,
-                        sl < 0 ? P.pool_slots : sl, &S.v_land[vs * 2 + ch]);
+            tma_load_pair(stage + (uint32_t)(4 * ch + (t >> 6) * nj + jj) * kAtom +
+                              (uint32_t)(t & 63) * 128u,
+                          &map_hi, ((int)rank * P.NV + 2 * ch + jj) * 64,
+                          sl < 0 ? P.pool_slots : sl, map_rank(smem_u32(bar), 0));
           }
           __syncwarp();
         }
+        if (!ok) break;
       }
-      if (!ok) break;
-      const int live = min(128, T.len - T.t0);       // rows that hold tokens
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.tok_empty[st]);
-#pragma unroll 1
-      for (int ch = 0; ch < nch; ++ch) {
-        const int nj = min(2, P.NV - 2 * ch);
-        ok = __all_sync(0xffffffffu, wait(&S.v_land[vs * 2 + ch], vpar));
-        if (!ok) break;
-        if (live < 128) {                             // 8 lanes a row
-#pragma unroll 1
-          for (int t = max(live, 0) + (vt >> 3); t < 128; t += 16)
-            for (int jj = 0; jj < nj; ++jj)
-              sts128(q_s + stage + (uint32_t)(4 * ch + (t >> 6) * nj + jj) * kAtom +
-                         (uint32_t)(t & 63) * 128u + (uint32_t)(vt & 7) * 16u,
-                     make_uint4(0u, 0u, 0u, 0u));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.v_full[vs * 2 + ch]);
-      }
-      if (!ok) break;
     }
-    if (vw == 0 && lane == 0)
+    if (vw == 0 && rank == 0 && lane == 0)
       for (int j = 0; j < 4; ++j)
-        if (armed >> j & 1) drain(&S.v_land[j], landing >> j & 1);
+        if (armed >> j & 1) drain(&S.v_ready[j], landing >> j & 1);
   } else if (!kExp && warp >= kVWarp0) {
     // ======================= V team =============================================================
     const int vt = tid - kVWarp0 * 32, tq = vt >> 2, sub = vt & 3;
@@ -1205,9 +1213,13 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
           sts128(row + (uint32_t)(((c + kCols / 8 * cg) ^ (r & 7)) << 4),
                  make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]));
       }
+      if constexpr (kExp) fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.p_full);
+      if (lane == 0) {
+        if constexpr (kExp) arrive_at(&S.p_ready, 0);
+        else mbar_arrive(&S.p_full);
+      }
       if (!last) continue;
 
       // ---- the piece's output ----
@@ -1424,6 +1436,7 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkWork& w, int dtype, c
     P.mark = w.mark;
     P.box = std::min(1 << a.page_shift, 64);
     P.pool_slots = w.pool_slots;
+    P.NK = std::min(kMaxK, room / 2);                // slots of two atoms
     if (!expanded_map(&hi, w.hi, P.NA, w.pool_slots, P.box) ||
         (split && !expanded_map(&lo, w.lo, P.NA, w.pool_slots, P.box)))
       return cudaErrorInvalidValue;
