@@ -22,15 +22,17 @@
 //   4-7    K team: own 64 tokens, packed codes -> 16-bit operand atoms (64 tokens x 64 features,
 //          128-byte swizzle) of a ring that the score MMA drains
 //   8-11   V team: all 128 tokens, this CTA's half of the latent features, for the output MMA
-//   12     MMA issuer (the leader CTA's)
+//   12     score MMAs (the leader CTA's)
 //   13     token warp: walks the cluster's pieces, resolves pages to slots, loads token scales,
 //          warms L2 with the rows, up to three blocks ahead of the others
 //   14     relay: passes the barriers of written operands on to the leader
+//   15     output MMAs (the leader CTA's)
 // Both teams stage the query rows at a piece's start.
 //
 // With expanded rows (kvk_chunk_expand.cu) nothing is converted here: warps 4-7 are a second set of
 // softmax warps (32 tokens a thread), warp 15 loads K, two atoms a ring slot, warp 8 V (TMA, counted
-// on the leader's barriers), warps 8-11 stage the query, and there is no relay.  What a block costs
+// on the leader's barriers), warps 8-11 stage the query, and warp 14 issues the output MMAs in the
+// relay's place.  What a block costs
 // beside its MMAs is the hand-over at the barriers (a skeleton without MMAs, loads and softmax took
 // 4200 cycles a block with a relay and single atoms), hence few and large steps.
 //
@@ -63,7 +65,7 @@ using namespace chunk;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kKWarp0 = 4, kVWarp0 = 8, kMmaWarp = 12, kTokWarp = 13, kRelayWarp = 14, kLoadWarp = 15;
+constexpr int kKWarp0 = 4, kVWarp0 = 8, kMmaWarp = 12, kTokWarp = 13, kRelayWarp = 14, kLoadWarp = 15;   // (see below)
 constexpr uint32_t kAtom = 8192;       // 64 rows x 128 bytes
 constexpr int kTokStages = 3;
 constexpr uint32_t kTmemCols = 512;
@@ -98,7 +100,7 @@ struct Shared {
   uint64_t k_full[kMaxK], k_ready[kMaxK], k_empty[kMaxK];
   uint64_t v_full[4], v_ready[4], v_empty[4];
   uint64_t q_full, q_ready, q_empty, q_local[4];
-  uint64_t s_full[2], p_full, p_ready, pv_done, x_bar, drain;
+  uint64_t s_full[2], s_free[2], p_full, p_ready, pv_done, x_bar, drain[2];
   int64_t scan[kWarps + 1];
   int64_t start_base;
   int32_t start_seq, start_k;
@@ -367,6 +369,50 @@ __device__ __noinline__ void stage_query(const TcChunk& P, Shared& S, uint32_t q
   }
 }
 
+// The rarely taken parts of the softmax warps, out of line: the steady loops of all roles share an
+// instruction cache that they only just fit.
+__device__ __noinline__ void rescale_o(uint32_t obase, int cols, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < cols; c += 32) {
+    float o[32];
+    tmem_ld32(obase + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] *= alpha;
+    tmem_st32(obase + c, o);
+  }
+  tmem_wait_st();
+}
+// Features f0 .. f0 + cols (those below d) of a row: fp32 sums (type < 0), or bf16 / f16 results.
+__device__ __noinline__ void write_o(uint32_t obase, int cols, int f0, int d, void* to, int type,
+                                     float inv) {
+#pragma unroll 1
+  for (int c = 0; c < cols; c += 32) {
+    float o[32];
+    tmem_ld32(obase + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {                // d is a multiple of 16
+      const int f = f0 + c + 8 * q;
+      if (f >= d) break;
+      if (type < 0) {
+        float* po = static_cast<float*>(to) + f;
+        *reinterpret_cast<float4*>(po) =
+            make_float4(o[8 * q], o[8 * q + 1], o[8 * q + 2], o[8 * q + 3]);
+        *reinterpret_cast<float4*>(po + 4) =
+            make_float4(o[8 * q + 4], o[8 * q + 5], o[8 * q + 6], o[8 * q + 7]);
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[k] = pack_out(type, o[8 * q + 2 * k] * inv, o[8 * q + 2 * k + 1] * inv);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(to) + f) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+}
+
 // Exclusive prefix of v over the block; *total gets the sum.  All threads call it.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* buf, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -399,6 +445,9 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
   constexpr bool kLo = kSplit<BITS, GROUP>;
   constexpr int kSoftWarps = kExp ? 8 : 4;
   constexpr int kStep = kExp ? 2 : 1;                 // atoms of a K ring slot
+  // the output MMAs' warp is the one that has no other work: the relay's with expanded rows, else
+  // the loads'
+  constexpr int kOutWarp = kExp ? kRelayWarp : kLoadWarp;
   extern __shared__ __align__(1024) uint8_t smem[];
   const ChunkArgs& a = P.a;
   Shared& S = *reinterpret_cast<Shared*>(smem + P.off_misc);
@@ -416,8 +465,8 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     S.abort_word = 0;
     for (int i = 0; i < kTokStages; ++i) {
       mbar_init(&S.tok_full[i], 1);
-      // softmax warps, loading or converting warps and relay, the leader's MMA warp
-      mbar_init(&S.tok_empty[i], kSoftWarps + (kExp ? 5 : 9) + (rank == 0 ? 1 : 0));
+      // softmax warps, loading or converting warps and relay, the leader's MMA warps
+      mbar_init(&S.tok_empty[i], kSoftWarps + (kExp ? 5 : 9) + (rank == 0 ? 2 : 0));
     }
     for (int i = 0; i < kMaxK; ++i) {
       mbar_init(&S.k_full[i], 4);
@@ -435,11 +484,14 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     mbar_init(&S.q_empty, 1);
     mbar_init(&S.s_full[0], 1);
     mbar_init(&S.s_full[1], 1);
+    mbar_init(&S.s_free[0], 2 * kSoftWarps);
+    mbar_init(&S.s_free[1], 2 * kSoftWarps);
     mbar_init(&S.p_full, kSoftWarps);
     mbar_init(&S.p_ready, kExp ? 2 * kSoftWarps : 2);
     mbar_init(&S.pv_done, 1);
     mbar_init(&S.x_bar, kSoftWarps);
-    mbar_init(&S.drain, 1);
+    mbar_init(&S.drain[0], 1);
+    mbar_init(&S.drain[1], 1);
     fence_mbar_init();
     // no partials of this cluster yet
     if (rank == 0) {
@@ -538,9 +590,14 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
   const Waiter wait{smem_u32(&S.abort_word), a.limit_ns};
   const int nch = (P.NV + 1) >> 1;       // output MMA steps over the features: 2 atoms, or the last 1
 
-  if (uniform(warp) == kMmaWarp) {
-    // ======================= MMA issuer =========================================================
-    if (rank == 0) {   // the whole warp, converged
+  // The warp index, and what a warp reads from shared memory to steer its MMAs, go through a
+  // shuffle: known to be the same in every lane, they and what follows from them stay in uniform
+  // registers, where the MMA's operands have to be.
+  if (uniform(warp) == kMmaWarp || uniform(warp) == kOutWarp) {
+    // ======================= MMA issuers: scores, outputs =======================================
+    // Two warps, each converged: what one spends between its MMAs (a wait, a commit: about 280
+    // cycles a step) the tensor cores spend on the other's.
+    if (rank == 0) {
       auto all = [&](uint64_t* b, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, wait(b, parity));
       };
@@ -551,23 +608,25 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       const uint32_t kl = ql + (P.off_k >> 4), pl = ql + (P.off_p >> 4);
       constexpr uint32_t kA = kAtom >> 4;             // an atom in descriptor units
       const uint32_t tmem = uniform(S.tmem_base);
+      const bool scores = uniform(warp) == kMmaWarp;
       int kslot = 0, pieces = 0;
       uint32_t kpar = 0;
-      int fl = 0;                                     // flags of the block before
       bool ok = true;
-      // block g: its score MMAs, then the output MMAs of block g - 1, whose softmax they cover
       for (int g = 0;; ++g) {
         const int st = g % kTokStages;
         ok = all(&S.tok_full[st], (g / kTokStages) & 1);
         if (!ok) break;
         const int now = uniform(*const_cast<volatile int32_t*>(&S.tok[st].flags));
         if (lane == 0) mbar_arrive(&S.tok_empty[st]);
-        if (!(now & kEnd)) {
+        if (now & kEnd) break;
+        if (scores) {
           if (now & kFirst) ok = all(&S.q_ready, pieces & 1);
+          ok = ok && all(&S.s_free[g & 1], ((g >> 1) & 1) ^ 1);
           if (!ok) break;
+          tc_fence_after();   // the softmax's reads of this S buffer
           const uint32_t scol = tmem + kSCol + 64u * (g & 1);
-          uint32_t acc = 0, qa = ql;
           const int atoms = P.NA * (kLo ? 2 : 1);
+          uint32_t acc = 0, qa = ql;
 #pragma unroll 1
           for (int i = 0; i < atoms; i += kStep) {
             ok = all(&S.k_ready[kslot], kpar);
@@ -592,15 +651,13 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
             commit_both(&S.q_empty);
             ++pieces;
           }
-        }
-        if (g > 0) {
-          // (the first block of a piece starts the sums anew)
-          ok = all(&S.p_ready, (g - 1) & 1);
+        } else {
+          ok = all(&S.p_ready, g & 1);
           if (!ok) break;
-          tc_fence_after();   // the softmax's reads of S and stores to O
-          const int vs = (g - 1) % P.NVS;
-          const uint32_t vpar = ((g - 1) / P.NVS) & 1;
-          const uint32_t acc = (fl & kFirst) ? 0u : 1u;
+          tc_fence_after();   // the softmax's stores to O
+          const int vs = g % P.NVS;
+          const uint32_t vpar = (g / P.NVS) & 1;
+          const uint32_t acc = (now & kFirst) ? 0u : 1u;   // a piece starts the sums anew
           uint32_t vb = vl + (uint32_t)(vs * 2 * P.NV) * kA;
 #pragma unroll 1
           for (int ch = 0; ch < nch; ++ch, vb += 4 * kA) {
@@ -615,13 +672,11 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
           if (!ok) break;
           commit_both(&S.pv_done);
         }
-        if (now & kEnd) break;
-        fl = now;
       }
       // every MMA and its arrivals are done before either CTA leaves
       __syncwarp();
-      commit_both(&S.drain);
-      drain(&S.drain, 0u);
+      commit_both(&S.drain[scores ? 0 : 1]);
+      drain(&S.drain[scores ? 0 : 1], 0u);
     }
   } else if (warp == kTokWarp) {
     // ======================= token warp: pieces, slots, scales ==================================
@@ -672,17 +727,22 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
             sc[i] = (kTok && sl[i] >= 0) ? __half2float(a.scales[sl[i]]) : 1.0f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int x = 32 * i + lane;
-            T.slot[x] = sl[i];
-            if constexpr (kTok) {
+            T.slot[32 * i + lane] = sl[i];
+            if constexpr (kTok) T.sc[32 * i + lane] = sc[i];
+            T.lsc[32 * i + lane] = sl[i] >= 0 ? mk[i] : -CUDART_INF_F;
+          }
+          if constexpr (kTok) {
+            // (the lane's own entries again, rolled: little code)
+#pragma unroll 1
+            for (int x = lane; x < 128; x += 32) {
+              const bool real = T.slot[x] >= 0;
+              const float v = T.sc[x];
               // an all-zero token (scale 0) keeps its score 0; its weight multiplies zeros, so
               // any positive scale serves
-              const float w = sc[i] == 0.0f ? 5.9604644775390625e-8f : sc[i];
-              T.sc[x] = sl[i] >= 0 ? sc[i] : 0.0f;
-              T.isc[x] = sl[i] >= 0 ? 1.0f / w : 0.0f;
-              T.lsc[x] = sl[i] >= 0 ? log2f(w) + mk[i] : -CUDART_INF_F;
-            } else {
-              T.lsc[x] = sl[i] >= 0 ? mk[i] : -CUDART_INF_F;
+              const float w = v == 0.0f ? 5.9604644775390625e-8f : v;
+              T.sc[x] = real ? v : 0.0f;
+              T.isc[x] = real ? __frcp_rn(w) : 0.0f;
+              T.lsc[x] += log2f(w);
             }
           }
           if (lane == 0) {
@@ -732,48 +792,76 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       }
     }
   } else if (warp == kRelayWarp) {
-    // ======================= relay ==============================================================
-    // One thread passes this CTA's full barriers, in the order of the MMAs, on to the leader.  It
-    // makes the proxy fence for the threads that wrote the operands, whose own would wait for
-    // all their loads in flight (measured 1600 cycles per atom of the K team), and the MMA
-    // issuer's for its MMAs.
+    // ======================= relay (converted rows) =============================================
+    // One thread passes this CTA's full barriers on to the leader: query and K in the order of the
+    // score MMAs, P and V in that of the output MMAs, whichever comes first.  It makes the proxy
+    // fence for the threads that wrote the operands, whose own would wait for all their loads in
+    // flight (measured 1600 cycles per atom of the K team).
     if (!kExp && lane == 0) {
+      const int atoms = P.NA * (kLo ? 2 : 1);
+      // score side: block gk, its barrier ik (-1: not entered, 0: query, 1 + atom); output side: gp,
+      // ip (0: P, 1 + step)
+      int gk = 0, ik = -1, kslot = 0, pieces = 0, gp = 0, ip = 0, end = 0x7FFFFFFF;
+      uint32_t kpar = 0;
+      uint64_t t0 = globaltimer();
+      int idle = 0;
       auto pass = [&](uint64_t* b, uint64_t* ready, uint32_t parity) -> bool {
-        if (!wait(b, parity)) return false;
+        if (!mbar_test(b, parity)) return false;
         fence_proxy_async_smem();
         arrive_at(ready, 0);
         return true;
       };
-      int kslot = 0, pieces = 0;
-      uint32_t kpar = 0;
-      bool ok = true;
-      for (int g = 0; ok; ++g) {
-        const int st = g % kTokStages;
-        ok = wait(&S.tok_full[st], (g / kTokStages) & 1);
-        if (!ok) break;
-        const int fl = *const_cast<volatile int32_t*>(&S.tok[st].flags);
-        mbar_arrive(&S.tok_empty[st]);
-        if (!(fl & kEnd)) {
-          if (fl & kFirst) ok = pass(&S.q_full, &S.q_ready, pieces & 1);
-          if (fl & kLast) ++pieces;
-#pragma unroll 1
-          for (int i = 0; ok && i < P.NA * (kLo ? 2 : 1); ++i) {
-            ok = pass(&S.k_full[kslot], &S.k_ready[kslot], kpar);
+      while (gk < end || gp < end) {
+        bool moved = false;
+        if (gk < end) {
+          if (ik < 0) {
+            const int st = gk % kTokStages;
+            if (mbar_test(&S.tok_full[st], (gk / kTokStages) & 1)) {
+              const int fl = *const_cast<volatile int32_t*>(&S.tok[st].flags);
+              mbar_arrive(&S.tok_empty[st]);
+              moved = true;
+              if (fl & kEnd) end = gk;
+              else ik = (fl & kFirst) ? 0 : 1;
+            }
+          } else if (ik == 0) {
+            if (pass(&S.q_full, &S.q_ready, pieces & 1)) {
+              ++pieces;
+              ik = 1;
+              moved = true;
+            }
+          } else if (pass(&S.k_full[kslot], &S.k_ready[kslot], kpar)) {
+            moved = true;
             if (++kslot == P.NK) {
               kslot = 0;
               kpar ^= 1;
             }
+            if (++ik > atoms) {
+              ik = -1;
+              ++gk;
+            }
           }
         }
-        if (ok && g > 0) {
-          ok = pass(&S.p_full, &S.p_ready, (g - 1) & 1);
-          const int vs = (g - 1) % P.NVS * 2;
-          const uint32_t vpar = ((g - 1) / P.NVS) & 1;
-#pragma unroll 1
-          for (int ch = 0; ok && ch < nch; ++ch)
-            ok = pass(&S.v_full[vs + ch], &S.v_ready[vs + ch], vpar);
+        if (gp < end) {
+          const int vs = gp % P.NVS * 2 + ip - 1;
+          if (ip == 0 ? pass(&S.p_full, &S.p_ready, gp & 1)
+                      : pass(&S.v_full[vs], &S.v_ready[vs], (gp / P.NVS) & 1)) {
+            moved = true;
+            if (++ip > nch) {
+              ip = 0;
+              ++gp;
+            }
+          }
         }
-        if (fl & kEnd) break;
+        if (moved) {
+          idle = 0;
+        } else if ((++idle & 63) == 0) {
+          if (abort_read(smem_u32(&S.abort_word))) break;
+          if (idle == 64) t0 = globaltimer();
+          else if (globaltimer() - t0 > a.limit_ns) {
+            wait_slow(&S.drain[0], 0u, smem_u32(&S.abort_word), 0ull);   // (stops both CTAs)
+            break;
+          }
+        }
       }
     }
   } else if (warp == kLoadWarp) {
@@ -1119,6 +1207,9 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
 #pragma unroll
       for (int i = 0; i < kCols; i += 32) tmem_ld32(sb + i, s + i);
       tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_at(&S.s_free[g & 1], 0);
       // w_t = z_t + log2 s_t, and its maximum over this half
       const float4* lsc4 = reinterpret_cast<const float4*>(T.lsc + col0);
       const float4* sc4 = reinterpret_cast<const float4*>(T.sc + col0);
@@ -1195,16 +1286,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         tc_fence_after();
       }
       if (!(fl & kFirst) && __any_sync(0xffffffffu, alpha != 1.0f)) {
-#pragma unroll 1
-        for (int c = 0; c < ocg; c += 32) {
-          float o[32];
-          tmem_ld32(obase + c, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= alpha;
-          tmem_st32(obase + c, o);
-        }
-        tmem_wait_st();
+        rescale_o(obase, ocg, alpha);
       }
       {
         const uint32_t row = p_s + (uint32_t)hh * kAtom + (uint32_t)r * 128u;
@@ -1239,33 +1321,10 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       const int part = (cluster * 2 + dest) * 128 + (int)rank * 64 + r;
       // a sum of zero: no token seen (or none that exists)
       const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
-      uint16_t* orow = static_cast<uint16_t*>(a.out) + (int64_t)row_q * a.o_st +
-                       (int64_t)row_h * a.o_sh;
-#pragma unroll 1
-      for (int c = 0; c < ocg; c += 32) {
-        float o[32];
-        tmem_ld32(obase + c, o);
-        tmem_wait_ld();
-        if (!row_ok) continue;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {                // d is a multiple of 16
-          const int f = f0 + c + 8 * q;
-          if (f >= a.d) break;
-          if (dest >= 0) {
-            float* po = P.w.o + (int64_t)part * a.d + f;
-            *reinterpret_cast<float4*>(po) =
-                make_float4(o[8 * q], o[8 * q + 1], o[8 * q + 2], o[8 * q + 3]);
-            *reinterpret_cast<float4*>(po + 4) =
-                make_float4(o[8 * q + 4], o[8 * q + 5], o[8 * q + 6], o[8 * q + 7]);
-          } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pack_out(P.q_bf16, o[8 * q + 2 * k] * inv, o[8 * q + 2 * k + 1] * inv);
-            *reinterpret_cast<uint4*>(orow + f) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      }
+      void* to = dest >= 0 ? static_cast<void*>(P.w.o + (int64_t)part * a.d)
+                           : static_cast<void*>(static_cast<uint16_t*>(a.out) +
+                                                (int64_t)row_q * a.o_st + (int64_t)row_h * a.o_sh);
+      write_o(obase, ocg, f0, row_ok ? a.d : 0, to, dest >= 0 ? -1 : P.q_bf16, inv);
       if (hh == 0 && cg == 0 && row_ok) {
         if (dest >= 0) {
           P.w.ml[2 * (int64_t)part] = m;
