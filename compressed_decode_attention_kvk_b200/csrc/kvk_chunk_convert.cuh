@@ -125,8 +125,9 @@ __device__ __forceinline__ bool nonfinite16(const uint32_t (&w)[8]) {
   return any != 0;
 }
 template <bool BF16>
-__device__ __noinline__ void replace_nonfinite(uint32_t* w, uint32_t with) {
+__device__ __forceinline__ void replace_nonfinite(uint32_t (&w)[8], uint32_t with) {
   const uint32_t e = BF16 ? 0x7F80u : 0x7C00u;
+#pragma unroll
   for (int i = 0; i < 8; ++i) {
     if ((w[i] & e) == e) w[i] = (w[i] & 0xFFFF0000u) | with;
     if (((w[i] >> 16) & e) == e) w[i] = (w[i] & 0xFFFFu) | (with << 16);

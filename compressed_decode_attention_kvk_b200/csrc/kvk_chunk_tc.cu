@@ -77,6 +77,13 @@ constexpr int kSmemLimit = 232448;
 constexpr int kMaxK = 12;              // slots of the K ring
 constexpr uint64_t kDrainLimitNs = 2000000000ull;
 
+constexpr uint32_t kLaunchRegs = 65536 / kThreads;
+template <uint32_t N>
+__device__ __forceinline__ void regs_set() {
+  if constexpr (N > kLaunchRegs) regs_inc<N>();
+  else if constexpr (N < kLaunchRegs) regs_dec<N>();
+}
+
 // One block of 128 tokens of a piece, published by the token warp.
 struct alignas(16) TokStage {
   int32_t slot[128];
@@ -237,9 +244,8 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* tmap, in
       : "memory");
 }
 
-// Bounded waits of one call: a wait that runs out stops both CTAs.  The loop is a function of its
-// own: inlined at every wait it pushes the roles' code out of the instruction cache.
-__device__ __noinline__ bool wait_slow(uint64_t* b, uint32_t parity, uint32_t abort_saddr,
+// Bounded waits of one call: a wait that runs out stops both CTAs.
+__device__ __forceinline__ bool wait_slow(uint64_t* b, uint32_t parity, uint32_t abort_saddr,
                                        uint64_t limit) {
   const uint64_t t0 = globaltimer();
   while (!mbar_try_hint(b, parity, 20000u)) {
@@ -286,18 +292,18 @@ __device__ __forceinline__ int blocks_of(int len, int count, int H, int flat0, i
   return max(1, (v + 127) >> 7);
 }
 
-// Query rows [r0, r1) of this CTA's 64, by one warp: two rows at a time.  A bf16 query for f16
+// Query rows [r0, r1) of this CTA's 64, by one warp: four rows' loads in flight.  A bf16 query for f16
 // operands is scaled by the power of two that brings its row's largest element into
 // [2^14, 2^15); other queries are copied.  A negative softmax scale flips the sign.
 template <bool OP_BF16>
-__device__ __noinline__ void stage_query(const TcChunk& P, Shared& S, uint32_t q_saddr,
+__device__ __forceinline__ void stage_query(const TcChunk& P, Shared& S, uint32_t q_saddr,
                                             const QueryTile& h, int rank, int r0, int r1) {
   const int lane = threadIdx.x & 31;
   const int chunks = P.NA * 8;                    // 16-byte chunks of 8 features
   const bool scale = !OP_BF16 && P.q_bf16;
   const uint32_t flip = P.a.sigma < 0.0f ? 0x80008000u : 0u;
   constexpr int kC = 3;                           // chunks a lane: up to 96 (768 features)
-  constexpr int kR = 2;
+  constexpr int kR = 4;
   const uint16_t* qlat = static_cast<const uint16_t*>(P.a.q_lat);
   const uint16_t* qrope = static_cast<const uint16_t*>(P.a.q_rope);
 #pragma unroll 1
@@ -369,9 +375,8 @@ __device__ __noinline__ void stage_query(const TcChunk& P, Shared& S, uint32_t q
   }
 }
 
-// The rarely taken parts of the softmax warps, out of line: the steady loops of all roles share an
-// instruction cache that they only just fit.
-__device__ __noinline__ void rescale_o(uint32_t obase, int cols, float alpha) {
+// The rarely taken parts of the softmax warps.
+__device__ __forceinline__ void rescale_o(uint32_t obase, int cols, float alpha) {
 #pragma unroll 1
   for (int c = 0; c < cols; c += 32) {
     float o[32];
@@ -384,7 +389,7 @@ __device__ __noinline__ void rescale_o(uint32_t obase, int cols, float alpha) {
   tmem_wait_st();
 }
 // Features f0 .. f0 + cols (those below d) of a row: fp32 sums (type < 0), or bf16 / f16 results.
-__device__ __noinline__ void write_o(uint32_t obase, int cols, int f0, int d, void* to, int type,
+__device__ __forceinline__ void write_o(uint32_t obase, int cols, int f0, int d, void* to, int type,
                                      float inv) {
 #pragma unroll 1
   for (int c = 0; c < cols; c += 32) {
@@ -588,12 +593,19 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   const Waiter wait{smem_u32(&S.abort_word), a.limit_ns};
+  // Registers: the block is launched with kLaunchRegs a thread (the host checks it); the last
+  // warpgroup gives some of its to the others, whose spills would go to L2 (shared memory takes
+  // the cache's place).
+  constexpr uint32_t kRegs0 = kExp ? 152 : 144, kRegs1 = 152, kRegs2 = kExp ? 128 : 144,
+                     kRegs3 = kExp ? 80 : 72;
+  static_assert(kRegs0 + kRegs1 + kRegs2 + kRegs3 <= 4 * kLaunchRegs, "register split");
   const int nch = (P.NV + 1) >> 1;       // output MMA steps over the features: 2 atoms, or the last 1
 
   // The warp index, and what a warp reads from shared memory to steer its MMAs, go through a
   // shuffle: known to be the same in every lane, they and what follows from them stay in uniform
   // registers, where the MMA's operands have to be.
   if (uniform(warp) == kMmaWarp || uniform(warp) == kOutWarp) {
+    regs_set<kRegs3>();
     // ======================= MMA issuers: scores, outputs =======================================
     // Two warps, each converged: what one spends between its MMAs (a wait, a commit: about 280
     // cycles a step) the tensor cores spend on the other's.
@@ -679,6 +691,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       drain(&S.drain[scores ? 0 : 1], 0u);
     }
   } else if (warp == kTokWarp) {
+    regs_set<kRegs3>();
     // ======================= token warp: pieces, slots, scales ==================================
     int seq = S.start_seq, k = S.start_k;
     int64_t base = S.start_base;
@@ -792,6 +805,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       }
     }
   } else if (warp == kRelayWarp) {
+    regs_set<kRegs3>();
     // ======================= relay (converted rows) =============================================
     // One thread passes this CTA's full barriers on to the leader: query and K in the order of the
     // score MMAs, P and V in that of the output MMAs, whichever comes first.  It makes the proxy
@@ -865,6 +879,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       }
     }
   } else if (warp == kLoadWarp) {
+    regs_set<kRegs3>();
     // ======================= K loads (expanded rows) ============================================
     int kslot = 0;
     uint32_t kpar = 1;
@@ -905,6 +920,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     if (kExp && rank == 0 && lane == 0)
       for (int j = 0; j < P.NK; ++j) drain(&S.k_ready[j], j < kslot ? kpar ^ 1 : kpar);
   } else if (kExp && warp >= kVWarp0) {
+    regs_set<kRegs2>();
     // ======================= V loads (expanded rows), query rows ================================
     const int vw = warp - kVWarp0;
     uint32_t armed = 0, landing = 0;                  // barriers used so far, and their last phase
@@ -964,6 +980,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       for (int j = 0; j < 4; ++j)
         if (armed >> j & 1) drain(&S.v_ready[j], landing >> j & 1);
   } else if (!kExp && warp >= kVWarp0) {
+    regs_set<kRegs2>();
     // ======================= V team =============================================================
     const int vt = tid - kVWarp0 * 32, tq = vt >> 2, sub = vt & 3;
     const int vw = warp - kVWarp0;
@@ -1040,6 +1057,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       if (!ok) break;
     }
   } else if (!kExp && warp >= kKWarp0) {
+    regs_set<kRegs1>();
     // ======================= K team =============================================================
     constexpr int D = 3;   // atoms whose loads are in flight
     const int kt = tid - kKWarp0 * 32, tq = kt >> 2, sub = kt & 3;
@@ -1158,6 +1176,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     }
   } else {
     // ======================= softmax ============================================================
+    regs_set<kRegs0>();
     // A row belongs to one thread per token half and, with expanded rows, column group: the
     // converting warps' place is then taken by a second set of softmax warps.
     constexpr int kCols = kExp ? 32 : 64;            // S columns (tokens) of a thread
@@ -1447,6 +1466,12 @@ template <int BITS, bool GROUP, bool kExp>
 cudaError_t launch(const TcChunk& P, const CUtensorMap& hi, const CUtensorMap& lo, size_t smem,
                    cudaStream_t st) {
   auto k = chunk_tc_kernel<BITS, GROUP, kExp>;
+  // the kernel hands registers from warpgroup to warpgroup: their number at launch is part of it
+  static const bool regs_ok = [&] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, k) == cudaSuccess && at.numRegs == (int)kLaunchRegs;
+  }();
+  if (!regs_ok) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   k<<<dim3(2 * P.w.G), dim3(kThreads), smem, st>>>(P, hi, lo);
