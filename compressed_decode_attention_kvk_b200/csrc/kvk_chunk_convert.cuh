@@ -140,13 +140,30 @@ struct Unit {
   uint32_t s;
 };
 
-// 16 elements of row `slot` from element e (a multiple of 16) on; slot < 0: not read
+// A token's packed row and, with group scales, its scales; a slot that does not exist (negative)
+// points at the pool's first row, whose values nothing may depend on.
+template <bool GROUP>
+struct Row {
+  const uint8_t* codes;
+  const unsigned short* scales;
+  bool real;
+};
+template <bool GROUP>
+__device__ __forceinline__ Row<GROUP> row_of(const ChunkArgs& a, int slot) {
+  Row<GROUP> r;
+  r.real = slot >= 0;
+  const int64_t at = max(slot, 0);
+  r.codes = a.codes + at * a.row_bytes;
+  r.scales = GROUP ? reinterpret_cast<const unsigned short*>(a.scales) + at * a.sg : nullptr;
+  return r;
+}
+
+// 16 elements of a row from element e (a multiple of 16) on
 template <int BITS, bool GROUP>
-__device__ __forceinline__ void load_unit(const ChunkArgs& a, int slot, int e,
+__device__ __forceinline__ void load_unit(const ChunkArgs& a, const Row<GROUP>& r, int e,
                                           Unit<BITS, GROUP>& u) {
   constexpr int RW = kRaw<BITS>;
-  if (slot < 0 || e < 0) return;
-  const uint8_t* p = a.codes + (int64_t)slot * a.row_bytes + e * kElemBits<BITS> / 8;
+  const uint8_t* p = r.codes + e * kElemBits<BITS> / 8;
   if constexpr (RW == 1) {
     u.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
   } else if constexpr (RW == 2) {
@@ -163,9 +180,28 @@ __device__ __forceinline__ void load_unit(const ChunkArgs& a, int slot, int e,
       u.w[4 * i + 3] = v.w;
     }
   }
-  if constexpr (GROUP)
-    u.s = __ldg(reinterpret_cast<const unsigned short*>(a.scales) + (int64_t)slot * a.sg +
-                e / a.group);
+  if constexpr (GROUP) u.s = __ldg(r.scales + e / a.group);
+}
+
+// The unit as operand words (hi, and lo where LO), zero unless `real`; a non-finite element becomes
+// `odd` (0x7FFF: NaN in either type) in the high part and zero in the low one.
+template <int BITS, bool GROUP, bool LO>
+__device__ __forceinline__ void operand16(const Unit<BITS, GROUP>& u, bool real, uint32_t odd,
+                                          uint32_t (&hi)[8], uint32_t (&lo)[8]) {
+  constexpr bool kBf16 = BITS == KVK_BITS_BF16;
+  convert16<BITS, GROUP, LO>(u.w, u.s, hi, lo);
+  if (!real) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      hi[i] = 0u;
+      if constexpr (LO) lo[i] = 0u;
+    }
+  } else if constexpr (kBf16 || GROUP) {
+    if (nonfinite16<kBf16>(hi)) {
+      replace_nonfinite<kBf16>(hi, odd);
+      if constexpr (LO) replace_nonfinite<kBf16>(lo, 0u);
+    }
+  }
 }
 
 }  // namespace chunk

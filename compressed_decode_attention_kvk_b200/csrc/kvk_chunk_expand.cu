@@ -51,7 +51,7 @@ chunk_expand_kernel(const __grid_constant__ ChunkArgs a, uint8_t* __restrict__ h
       uint32_t hi[8], lo[8];
       if (e >= 0) {
         Unit<BITS, GROUP> v;
-        load_unit<BITS, GROUP>(a, sl, e, v);
+        load_unit<BITS, GROUP>(a, row_of<GROUP>(a, sl), e, v);
         convert16<BITS, GROUP, kLo>(v.w, v.s, hi, lo);
         if constexpr (kBf16 || GROUP) {
           if (nonfinite16<kBf16>(hi)) {

@@ -74,7 +74,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;          // growth of a row's maximum that its reference lets pass
 constexpr int kSmemLimit = 232448;
-constexpr int kMaxK = 12;              // slots of the K ring
+constexpr int kMaxK = 8;               // slots of the K ring, two atoms each
 constexpr uint64_t kDrainLimitNs = 2000000000ull;
 
 constexpr uint32_t kLaunchRegs = 65536 / kThreads;
@@ -449,7 +449,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
   constexpr bool kTok = !GROUP && !kBf16;             // one scale per token
   constexpr bool kLo = kSplit<BITS, GROUP>;
   constexpr int kSoftWarps = kExp ? 8 : 4;
-  constexpr int kStep = kExp ? 2 : 1;                 // atoms of a K ring slot
+  constexpr int kStep = 2;                            // atoms of a K ring slot
   // the output MMAs' warp is the one that has no other work: the relay's with expanded rows, else
   // the loads'
   constexpr int kOutWarp = kExp ? kRelayWarp : kLoadWarp;
@@ -645,11 +645,9 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
             if (!ok) break;
             const uint32_t kb = kl + (uint32_t)(kslot * kStep) * kA;
             mma2x4(scol, qa, kb, 2u, hk, hk, P.idesc_s, acc);
-            if (!kLo || (kStep == 1 && (i & 1))) qa += kA;
-            if (kStep == 2) {        // the next atom, or the low part of the same elements
-              if (i + 1 < atoms) mma2x4(scol, qa, kb + kA, 2u, hk, hk, P.idesc_s, 1u);
-              qa += kA;
-            }
+            if (!kLo) qa += kA;      // the next atom, or the low part of the same elements
+            if (i + 1 < atoms) mma2x4(scol, qa, kb + kA, 2u, hk, hk, P.idesc_s, 1u);
+            qa += kA;
             commit_both(&S.k_empty[kslot]);
             acc = 1;
             if (++kslot == P.NK) {
@@ -812,8 +810,8 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     // fence for the threads that wrote the operands, whose own would wait for all their loads in
     // flight (measured 1600 cycles per atom of the K team).
     if (!kExp && lane == 0) {
-      const int atoms = P.NA * (kLo ? 2 : 1);
-      // score side: block gk, its barrier ik (-1: not entered, 0: query, 1 + atom); output side: gp,
+      const int steps = (P.NA * (kLo ? 2 : 1) + kStep - 1) / kStep;
+      // score side: block gk, its barrier ik (-1: not entered, 0: query, 1 + step); output side: gp,
       // ip (0: P, 1 + step)
       int gk = 0, ik = -1, kslot = 0, pieces = 0, gp = 0, ip = 0, end = 0x7FFFFFFF;
       uint32_t kpar = 0;
@@ -849,7 +847,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
               kslot = 0;
               kpar ^= 1;
             }
-            if (++ik > atoms) {
+            if (++ik > steps) {
               ik = -1;
               ++gk;
             }
@@ -992,16 +990,18 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       const TokStage& T = S.tok[st];
       const int fl = T.flags;
       if (fl & kEnd) break;
-      int sl[4];
+      Row<GROUP> row[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) sl[u] = T.slot[tq + 32 * u];
-      Unit<BITS, GROUP> buf[2][4];
-      auto load = [&](int j, Unit<BITS, GROUP> (&b)[4]) {
+      for (int u = 0; u < 4; ++u) row[u] = row_of<GROUP>(a, T.slot[tq + 32 * u]);
+      Unit<BITS, GROUP> cur[4], nxt[4];
+      auto load = [&](int j, Unit<BITS, GROUP> (&to)[4]) {
         const int e = unit_elem(P, (int)rank * P.NV + j, sub);
+        if (e >= 0) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) load_unit<BITS, GROUP>(a, sl[u], e, b[u]);
+          for (int u = 0; u < 4; ++u) load_unit<BITS, GROUP>(a, row[u], e, to[u]);
+        }
       };
-      load(0, buf[0]);
+      load(0, cur);
       if (fl & kFirst) {
         if (T.piece > 0) ok = wait(&S.q_empty, (T.piece - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
@@ -1020,157 +1020,132 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       const uint32_t vpar = ((g / P.NVS) & 1) ^ 1;
       const uint32_t stage = v_s + (uint32_t)(vs * 2 * P.NV) * kAtom;
 #pragma unroll 1
-      for (int j0 = 0; j0 < P.NV; j0 += 2) {
-        const int ch = j0 >> 1;
-        const bool two = j0 + 2 <= P.NV;
-#pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {
-          const int j = j0 + jj;
-          if (j >= P.NV) break;
-          if (j + 1 < P.NV) load(j + 1, buf[(jj + 1) & 1]);
-          if (jj == 0) {
-            ok = __all_sync(0xffffffffu, wait(&S.v_empty[vs * 2 + ch], vpar));
-            if (!ok) break;
-          }
-          const int e = unit_elem(P, (int)rank * P.NV + j, sub);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t hi[8], lo[8];
-            if (sl[u] >= 0 && e >= 0) {
-              convert16<BITS, GROUP, false>(buf[jj & 1][u].w, buf[jj & 1][u].s, hi, lo);
-              if constexpr (kBf16 || GROUP) {
-                if (nonfinite16<kBf16>(hi)) replace_nonfinite<kBf16>(hi, 0u);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) hi[i] = 0u;
-            }
-            // [token half][atom of the step][64 tokens]
-            const uint32_t atom = stage + (uint32_t)(4 * ch + (u >> 1) * (two ? 2 : 1) + jj) * kAtom;
-            store_unit(atom, tq + 32 * (u & 1), sub, hi);
-          }
+      for (int j = 0; j < P.NV; ++j) {
+        const int ch = j >> 1, jj = j & 1, nj = min(2, P.NV - 2 * ch);
+        if (j + 1 < P.NV) load(j + 1, nxt);
+        if (jj == 0) {
+          ok = __all_sync(0xffffffffu, wait(&S.v_empty[vs * 2 + ch], vpar));
+          if (!ok) break;
         }
-        if (!ok) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.v_full[vs * 2 + ch]);
+        const int e = unit_elem(P, (int)rank * P.NV + j, sub);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t hi[8], lo[8];
+          operand16<BITS, GROUP, false>(cur[u], e >= 0 && (kTok || row[u].real), 0u, hi, lo);
+          // [token half][atom of the step][64 tokens]
+          store_unit(stage + (uint32_t)(4 * ch + (u >> 1) * nj + jj) * kAtom, tq + 32 * (u & 1), sub, hi);
+        }
+        if (jj + 1 == nj) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.v_full[vs * 2 + ch]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) cur[u] = nxt[u];
       }
       if (!ok) break;
     }
   } else if (!kExp && warp >= kKWarp0) {
     regs_set<kRegs1>();
     // ======================= K team =============================================================
-    constexpr int D = 3;   // atoms whose loads are in flight
+    // A ring slot is two atoms: two of the row's, or the high and the low part of one.  The next
+    // slot's rows are loaded while this one's are converted.
+    constexpr int kPer = kLo ? 1 : 2;             // atoms of the row in a slot
     const int kt = tid - kKWarp0 * 32, tq = kt >> 2, sub = kt & 3;
     const int kw = warp - kKWarp0;
+    const int steps = (P.NA + kPer - 1) / kPer;
     int kslot = 0;
     uint32_t kpar = 1;
-    bool ok = true;
+    bool ok = true, last = false;
     int g = 0;             // next block to be taken from the token ring
+    Row<GROUP> row[2];     // of the block whose rows are loaded next
+    Unit<BITS, GROUP> cur[kPer][2], nxt[kPer][2];
+    bool real[2], next_real[2];
+    auto take = [&]() -> bool {
+      const int s1 = g % kTokStages;
+      if (!__all_sync(0xffffffffu, wait(&S.tok_full[s1], (g / kTokStages) & 1))) return false;
+      const TokStage& T = S.tok[s1];
+      last = (T.flags & kLast) != 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        row[u] = row_of<GROUP>(a, T.slot[64 * (int)rank + tq + 32 * u]);
+        next_real[u] = row[u].real;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.tok_empty[s1]);
+      ++g;
+      return true;
+    };
+    auto load = [&](int step, Unit<BITS, GROUP> (&to)[kPer][2]) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int at = step * kPer + j;
+        const int e = at < P.NA ? unit_elem(P, at, sub) : -1;
+        if (e >= 0) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) load_unit<BITS, GROUP>(a, row[u], e, to[j][u]);
+        }
+      }
+    };
     for (;;) {             // one piece
-      int st = g % kTokStages;
+      const int st = g % kTokStages;
       ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], (g / kTokStages) & 1));
       if (!ok) break;
       if (S.tok[st].flags & kEnd) break;
-      // prefetch cursor: atom pa of the block whose slots are in ps; more: further atoms exist
-      int ps[2], pa = 0;
-      bool more = true, last = false;
-      const int piece = S.tok[st].piece;
-      const QueryTile head = {S.tok[st].row0, S.tok[st].flat0, S.tok[st].rows, piece};
-      auto take = [&]() -> bool {   // the block of ring entry g into the cursor
-        const int s1 = g % kTokStages;
-        if (!__all_sync(0xffffffffu, wait(&S.tok_full[s1], (g / kTokStages) & 1))) return false;
-        const TokStage& T = S.tok[s1];
-        last = (T.flags & kLast) != 0;
-        ps[0] = T.slot[64 * (int)rank + tq];
-        ps[1] = T.slot[64 * (int)rank + tq + 32];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.tok_empty[s1]);
-        ++g;
-        return true;
-      };
+      const QueryTile head = {S.tok[st].row0, S.tok[st].flat0, S.tok[st].rows, S.tok[st].piece};
       ok = take();
       if (!ok) break;
-      Unit<BITS, GROUP> buf[D][2];
-      int be[D];            // element index of the buffered unit (-1: padding), or -2: none
-      bool bz[D][2];        // its token exists
-      auto fetch = [&](int& e_out, bool (&z)[2], Unit<BITS, GROUP> (&b)[2]) -> bool {
-        if (pa == P.NA) {
-          if (last) more = false;
-          else {
-            if (!take()) return false;
-            pa = 0;
-          }
-        }
-        if (!more) {
-          e_out = -2;
-          return true;
-        }
-        const int e = unit_elem(P, pa, sub);
-        e_out = e;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          z[u] = ps[u] >= 0;
-          load_unit<BITS, GROUP>(a, ps[u], e, b[u]);
-        }
-        ++pa;
-        return true;
-      };
-#pragma unroll
-      for (int u = 0; u < D; ++u)
-        if (ok) ok = fetch(be[u], bz[u], buf[u]);
-      if (!ok) break;
-      if (piece > 0) ok = __all_sync(0xffffffffu, wait(&S.q_empty, (piece - 1) & 1));
+      load(0, cur);
+      real[0] = next_real[0], real[1] = next_real[1];
+      if (head.piece > 0) ok = __all_sync(0xffffffffu, wait(&S.q_empty, (head.piece - 1) & 1));
       if (!ok) break;
       stage_query<kBf16>(P, S, q_s, head, (int)rank, kw * 8, kw * 8 + 8);
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&S.q_local[piece & 3]);
+        mbar_arrive(&S.q_local[head.piece & 3]);
         mbar_arrive(&S.q_full);
       }
-      bool done = false;
-      while (!done) {
+      int step = 0;
+      for (bool more = true; more;) {
+        // the rows after these
+        int next = step + 1;
+        if (next < steps) {
+          load(next, nxt);
+        } else if (last) {
+          more = false;
+        } else {
+          next = 0;
+          ok = take();
+          if (!ok) break;
+          load(0, nxt);
+        }
+        ok = __all_sync(0xffffffffu, wait(&S.k_empty[kslot], kpar));
+        if (!ok) break;
+        const uint32_t slot = k_s + (uint32_t)(2 * kslot) * kAtom;
 #pragma unroll
-        for (int x = 0; x < D; ++x) {
-          // (the end is the same in every lane: it follows the ring's flags)
-          if (be[x] == -2) {
-            done = true;
-            break;
-          }
-          uint32_t hi[2][8], lo[2][8];
+        for (int j = 0; j < kPer; ++j) {
+          const int at = step * kPer + j;
+          if (at >= P.NA) break;
+          const int e = unit_elem(P, at, sub);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            if (bz[x][u] && be[x] >= 0) {
-              convert16<BITS, GROUP, kLo>(buf[x][u].w, buf[x][u].s, hi[u], lo[u]);
-              if constexpr (kBf16 || GROUP) {
-                if (nonfinite16<kBf16>(hi[u])) {
-                  replace_nonfinite<kBf16>(hi[u], 0x7FFFu);
-                  if constexpr (kLo) replace_nonfinite<kBf16>(lo[u], 0u);
-                }
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) hi[u][i] = 0u, lo[u][i] = 0u;
-            }
+            uint32_t hi[8], lo[8];
+            operand16<BITS, GROUP, kLo>(cur[j][u], e >= 0 && (kTok || real[u]), 0x7FFFu, hi, lo);
+            store_unit(slot + (uint32_t)j * kAtom, tq + 32 * u, sub, hi);
+            if constexpr (kLo) store_unit(slot + kAtom, tq + 32 * u, sub, lo);
           }
-          ok = fetch(be[x], bz[x], buf[x]);
-          if (!ok) break;
-#pragma unroll
-          for (int part = 0; part < (kLo ? 2 : 1); ++part) {
-            ok = __all_sync(0xffffffffu, wait(&S.k_empty[kslot], kpar));
-            if (!ok) break;
-            const uint32_t atom = k_s + (uint32_t)kslot * kAtom;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) store_unit(atom, tq + 32 * u, sub, part ? lo[u] : hi[u]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.k_full[kslot]);
-            if (++kslot == P.NK) {
-              kslot = 0;
-              kpar ^= 1;
-            }
-          }
-          if (!ok) break;
         }
-        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.k_full[kslot]);
+        if (++kslot == P.NK) {
+          kslot = 0;
+          kpar ^= 1;
+        }
+        step = next;
+        if (next == 0) real[0] = next_real[0], real[1] = next_real[1];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) cur[j][u] = nxt[j][u];
       }
       if (!ok) break;
     }
@@ -1497,9 +1472,9 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkWork& w, int dtype, c
   P.NV = P.NL / 2;
   P.NVS = P.NV <= 2 ? 2 : 1;
   const int room = (int)((kSmemLimit - (int)sizeof(Shared)) / (int)kAtom) - P.NA - 2 * P.NV * P.NVS - 2;
-  P.NK = std::min(kMaxK, room);
+  P.NK = std::min(kMaxK, room / 2);   // slots of two atoms
   P.off_k = (uint32_t)P.NA * kAtom;
-  P.off_v = P.off_k + (uint32_t)P.NK * kAtom;
+  P.off_v = P.off_k + (uint32_t)(2 * P.NK) * kAtom;
   P.off_p = P.off_v + (uint32_t)(2 * P.NV * P.NVS) * kAtom;
   P.off_misc = P.off_p + 2 * kAtom;
   const bool bf = a.b == KVK_BITS_BF16;
@@ -1520,7 +1495,6 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkWork& w, int dtype, c
     P.mark = w.mark;
     P.box = std::min(1 << a.page_shift, 64);
     P.pool_slots = w.pool_slots;
-    P.NK = std::min(kMaxK, room / 2);                // slots of two atoms
     if (!expanded_map(&hi, w.hi, P.NA, w.pool_slots, P.box) ||
         (split && !expanded_map(&lo, w.lo, P.NA, w.pool_slots, P.box)))
       return cudaErrorInvalidValue;
