@@ -1357,54 +1357,103 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
 // join of the row tiles that several clusters worked on
 // ---------------------------------------------------------------------------------------
 constexpr int kMergeWarps = 8;
+constexpr int kMergeRounds = 4;   // pieces of a tile in rounds of 32 lanes: up to 127 clusters
 
-// CTA (g, y): if the last piece of cluster g began a tile it did not finish, rows y, y +
-// gridDim.y, ... (one a warp) of that tile, whose further pieces are the first ones of clusters
-// g + 1, ... up to the one that ends it.
+// CTA (g, y): if the last piece of cluster g began a tile it did not finish, rows 8 y .. 8 y + 7
+// (one a warp) of that tile, whose further pieces are the first ones of clusters g + 1, ... up to
+// the one that ends it.  A lane holds reference and sum of one piece a round; the outputs are then
+// added up piece by piece, 4 features a lane and 128, their loads independent of one another.
 __global__ void __launch_bounds__(kMergeWarps * 32)
 chunk_merge_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ ChunkWork w,
                    int q_bf16) {
+  griddep_wait();                        // the partials are complete and visible
   const int g = blockIdx.x, lane = threadIdx.x & 31;
   const ChunkPartial h = w.head[2 * g + 1];
   if (!h.valid) return;
   const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
   const int flat = h.flat0 + row;
   if (flat >= h.rows) return;
-  int end = g + 1;                       // pieces: (g, 1), (g + 1, 0), ..., (end - 1, 0)
-  for (bool done = false; !done && end < w.G; ++end) {
-    const ChunkPartial& x = w.head[2 * end];
-    if (x.valid && (x.seq != h.seq || x.flat0 != h.flat0)) break;
-    done = x.valid && x.b1 == x.nblk;
+  // piece i of the tile: cluster g + i, its first slot (cluster g: its second)
+  auto slot = [&](int i) { return (int64_t)(2 * (g + i) + (i == 0 ? 1 : 0)) * 128 + row; };
+  float m[kMergeRounds], l[kMergeRounds];
+  int n = 0;                             // pieces, those of clusters without one among them
+  bool open = true;
+#pragma unroll
+  for (int r = 0; r < kMergeRounds; ++r) {
+    m[r] = -CUDART_INF_F;
+    l[r] = 0.0f;
+    if (!open) continue;
+    const int i = 32 * r + lane, c = g + i;
+    bool in = i == 0, stop = c >= w.G, ends = false;
+    if (i > 0 && !stop) {
+      const ChunkPartial& x = w.head[2 * c];
+      in = x.valid != 0;
+      stop = in && (x.seq != h.seq || x.flat0 != h.flat0);
+      ends = in && !stop && x.b1 == x.nblk;
+    }
+    const unsigned before = __ballot_sync(0xffffffffu, stop), fin = __ballot_sync(0xffffffffu, ends);
+    int take = 32;                       // lanes of this round that belong to the tile
+    if (fin) take = __ffs(fin);
+    if (before) take = min(take, __ffs(before) - 1);
+    open = take == 32 && !(fin >> 31);
+    n = 32 * r + take;
+    if (in && lane < take) {
+      const float2 v = *reinterpret_cast<const float2*>(w.ml + 2 * slot(i));
+      m[r] = v.x;
+      l[r] = v.y;
+    }
   }
-  auto slot = [&](int c) { return (int64_t)(2 * c + (c == g ? 1 : 0)) * 128 + row; };
-  auto live = [&](int c) { return c == g || w.head[2 * c].valid; };
   float M = -CUDART_INF_F;
-  for (int c = g; c < end; ++c)
-    if (live(c)) M = fmaxf(M, w.ml[2 * slot(c)]);
+#pragma unroll
+  for (int r = 0; r < kMergeRounds; ++r) M = fmaxf(M, m[r]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.0f;
+#pragma unroll
+  for (int r = 0; r < kMergeRounds; ++r) {
+    m[r] = m[r] == -CUDART_INF_F ? 0.0f : exp2f(m[r] - M);   // (NaN stays NaN)
+    L += m[r] * l[r];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  float4 acc[4];                          // d <= 512
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int r = 0; r < kMergeRounds; ++r) {
+    const int top = min(32, n - 32 * r);
+#pragma unroll 4
+    for (int i = 0; i < top; ++i) {
+      const float x = __shfl_sync(0xffffffffu, m[r], i);
+      if (x == 0.0f) continue;            // no piece, or no weight
+      const float* o = w.o + slot(32 * r + i) * a.d;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int f = 128 * k + 4 * lane;
+        if (f < a.d) {
+          const float4 v = *reinterpret_cast<const float4*>(o + f);
+          acc[k].x = fmaf(x, v.x, acc[k].x);
+          acc[k].y = fmaf(x, v.y, acc[k].y);
+          acc[k].z = fmaf(x, v.z, acc[k].z);
+          acc[k].w = fmaf(x, v.w, acc[k].w);
+        }
+      }
+    }
+  }
   const int j = flat / a.H, hd = flat - j * a.H;
   uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(h.row0 + j) * a.o_st +
                   (int64_t)hd * a.o_sh;
-  const float ref = M == -CUDART_INF_F ? 0.0f : M;
-  float l = 0.0f;
-  for (int c = g; c < end; ++c)
-    if (live(c)) l += exp2f(w.ml[2 * slot(c)] - ref) * w.ml[2 * slot(c) + 1];
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  for (int f = 4 * lane; f < a.d; f += 128) {
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = g; c < end; ++c) {
-      if (!live(c)) continue;
-      const float x = exp2f(w.ml[2 * slot(c)] - ref);
-      const float4 o = *reinterpret_cast<const float4*>(w.o + slot(c) * a.d + f);
-      acc.x = fmaf(x, o.x, acc.x);
-      acc.y = fmaf(x, o.y, acc.y);
-      acc.z = fmaf(x, o.z, acc.z);
-      acc.w = fmaf(x, o.w, acc.w);
-    }
-    *reinterpret_cast<uint2*>(out + f) = make_uint2(pack_out(q_bf16, acc.x * inv, acc.y * inv),
-                                                    pack_out(q_bf16, acc.z * inv, acc.w * inv));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int f = 128 * k + 4 * lane;
+    if (f < a.d)
+      *reinterpret_cast<uint2*>(out + f) =
+          make_uint2(pack_out(q_bf16, acc[k].x * inv, acc[k].y * inv),
+                     pack_out(q_bf16, acc[k].z * inv, acc[k].w * inv));
   }
   if (a.lse && lane == 0)
-    a.lse[(int64_t)(h.row0 + j) * a.H + hd] = l == 0.0f ? -CUDART_INF_F : kLn2 * (M + log2f(l));
+    a.lse[(int64_t)(h.row0 + j) * a.H + hd] = L == 0.0f ? -CUDART_INF_F : kLn2 * (M + log2f(L));
 }
 
 __host__ constexpr uint32_t idesc_of(bool bf16, int N, bool b_mn) {
@@ -1484,7 +1533,7 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkWork& w, int dtype, c
   P.q_bf16 = dtype == KVK_BF16;
   const size_t smem = P.off_misc + sizeof(Shared);
   // the prologue's prefix sums use the rings' memory
-  if (P.NK < 2 || smem > (size_t)kSmemLimit || (size_t)(a.batch + 1) * 4 > P.off_misc)
+  if (w.G >= 32 * kMergeRounds || P.NK < 2 || smem > (size_t)kSmemLimit || (size_t)(a.batch + 1) * 4 > P.off_misc)
     return cudaErrorInvalidValue;
   CUtensorMap hi, lo;
   memset(&hi, 0, sizeof(hi));
@@ -1518,8 +1567,10 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkWork& w, int dtype, c
     else if (a.b == 16) e = launch<16, false, false>(P, hi, lo, smem, st);
   }
   if (e != cudaSuccess) return e;
-  chunk_merge_kernel<<<dim3(w.G, 128 / kMergeWarps), dim3(kMergeWarps * 32), 0, st>>>(a, w, P.q_bf16);
-  return cudaGetLastError();
+  // a programmatic dependent: its CTAs are in place when the partials are
+  e = launch_pdl(chunk_merge_kernel, dim3(w.G, 128 / kMergeWarps), dim3(kMergeWarps * 32), 0, st, a, w,
+                 P.q_bf16);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 size_t chunk_workspace(const AnchorDesc& A, int d_rope, int group, int64_t slots, int G, bool expand,
