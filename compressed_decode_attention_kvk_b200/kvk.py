@@ -184,9 +184,14 @@ def kvk_destroy(handle):
         _lib_handle().kvk_destroy(handle)
 
 
-def kvk_get_layer_info(handle, layer) -> dict:
+def _layer_info(handle, layer) -> LayerInfo:
     info = LayerInfo()
     _check("kvk_get_layer_info", _lib_handle().kvk_get_layer_info(handle, layer, ctypes.byref(info)))
+    return info
+
+
+def kvk_get_layer_info(handle, layer) -> dict:
+    info = _layer_info(handle, layer)
     return {f: getattr(info, f) for f, _ in LayerInfo._fields_}
 
 
@@ -352,51 +357,93 @@ def kvk_absorb(x, w, y, stream=None):
     return y
 
 
+# The paged calls are short: their checks are written out (no helper call, no ctypes object per
+# argument, the raw stream instead of a Stream object, which alone takes 3 us to make).  Every
+# tensor has to be on the current device: the library launches there.
+
+def _bad(t, name, dtypes, device):
+    """The error of a tensor that a paged call cannot take."""
+    if not t.is_cuda:
+        return ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        return ValueError(f"{name} is on cuda:{t.get_device()}, the current device is "
+                          f"cuda:{device}")
+    if dtypes and t.dtype not in dtypes:
+        return ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    return ValueError(f"{name} must be contiguous")
+
+
+def _current_device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return torch.cuda.current_device()
+
+
+def _raw_stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+_I32 = (torch.int32,)
+_KV_TYPES = (torch.float32, torch.bfloat16)
+
+
 def kvk_paged_plan(handle, cached, new, free_pages, free_count, block_table, page_tokens, max_new,
                    seq_lens, q_start, slots, positions, free_count_out, stream=None):
     """The pages and slots of a step's new tokens.  cached, new int32 [B]; free_pages int32 [F]
     with free_count int32 [1] valid entries; block_table int32 [B, pages] (updated in place);
     results: seq_lens int32 [B], q_start int32 [B + 1], slots and positions (or None) int32
     [>= max_new], free_count_out int32 [1] (may be free_count)."""
-    for t, name in ((cached, "cached"), (new, "new"), (free_pages, "free_pages"),
-                    (free_count, "free_count"), (block_table, "block_table"),
-                    (seq_lens, "seq_lens"), (q_start, "q_start"), (slots, "slots"),
-                    (positions, "positions"), (free_count_out, "free_count_out")):
-        _need_cuda(t, name, (torch.int32,))
-        if t is not None and name != "block_table" and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+    i32, dev = torch.int32, _current_device(cached, "cached")
+    tensors = (cached, new, free_pages, free_count, seq_lens, q_start, slots, free_count_out)
+    for k, t in enumerate(tensors):
+        if not (t.get_device() == dev and t.dtype is i32 and t.is_contiguous()):
+            raise _bad(t, ("cached", "new", "free_pages", "free_count", "seq_lens", "q_start",
+                           "slots", "free_count_out")[k], _I32, dev)
+    if positions is not None and not (positions.get_device() == dev and positions.dtype is i32 and
+                                      positions.is_contiguous()):
+        raise _bad(positions, "positions", _I32, dev)
+    if not (block_table.get_device() == dev and block_table.dtype is i32):
+        raise _bad(block_table, "block_table", _I32, dev)
     if block_table.dim() != 2 or block_table.stride(1) != 1:
         raise ValueError("block_table must be [batch, pages] with contiguous rows")
     B = cached.numel()
-    if new.numel() != B or block_table.shape[0] != B or seq_lens.numel() < B or \
-            q_start.numel() < B + 1 or slots.numel() < max_new or \
-            (positions is not None and positions.numel() < max_new) or \
+    rows, pages = block_table.shape
+    if new.numel() != B or rows != B or seq_lens.numel() < B or q_start.numel() < B + 1 or \
+            slots.numel() < max_new or (positions is not None and positions.numel() < max_new) or \
             free_count.numel() < 1 or free_count_out.numel() < 1:
         raise ValueError("sizes of the plan's tensors do not match the batch and max_new")
     st = _lib_handle().kvk_paged_plan(
-        handle, _ptr(cached), _ptr(new), B, _ptr(free_pages), _ptr(free_count),
-        free_pages.numel(), page_tokens, _ptr(block_table), block_table.shape[1],
-        _row_stride(block_table), max_new, _ptr(seq_lens), _ptr(q_start), _ptr(slots),
-        _ptr(positions), _ptr(free_count_out), _stream(stream))
-    _check("kvk_paged_plan", st)
+        handle, cached.data_ptr(), new.data_ptr(), B, free_pages.data_ptr(),
+        free_count.data_ptr(), free_pages.numel(), page_tokens, block_table.data_ptr(), pages,
+        block_table.stride(0) if B > 1 else pages, max_new, seq_lens.data_ptr(),
+        q_start.data_ptr(), slots.data_ptr(),
+        None if positions is None else positions.data_ptr(), free_count_out.data_ptr(),
+        _raw_stream(stream, dev))
+    if st:
+        raise KvkError("kvk_paged_plan", st)
 
 
 def kvk_paged_write(handle, layer, c_kv, k_rope, slots, stream=None):
     """c_kv [N, >=d], k_rope [N, d_rope] (fp32 or bf16, CUDA, last dim contiguous) quantised to
     slots int32 [>= N] of the layer's pool (negative: skipped)."""
-    _need_cuda(c_kv, "c_kv", (torch.float32, torch.bfloat16))
-    _need_cuda(k_rope, "k_rope", (c_kv.dtype,))
-    _need_cuda(slots, "slots", (torch.int32,))
-    if c_kv.dim() != 2 or k_rope.dim() != 2 or \
-            any(t.shape[1] > 1 and t.stride(1) != 1 for t in (c_kv, k_rope)):
+    dtype, dev = c_kv.dtype, _current_device(c_kv, "c_kv")
+    if not (c_kv.get_device() == dev and dtype in _KV_TYPES):
+        raise _bad(c_kv, "c_kv", _KV_TYPES, dev)
+    if not (k_rope.get_device() == dev and k_rope.dtype is dtype):
+        raise _bad(k_rope, "k_rope", (dtype,), dev)
+    if not (slots.get_device() == dev and slots.dtype is torch.int32 and slots.is_contiguous()):
+        raise _bad(slots, "slots", _I32, dev)
+    if c_kv.dim() != 2 or k_rope.dim() != 2 or (c_kv.shape[1] > 1 and c_kv.stride(1) != 1) or \
+            (k_rope.shape[1] > 1 and k_rope.stride(1) != 1):
         raise ValueError("c_kv / k_rope must be [tokens, width] with contiguous width")
-    if k_rope.shape[0] != c_kv.shape[0] or slots.numel() < c_kv.shape[0] or \
-            not slots.is_contiguous():
+    N = c_kv.shape[0]
+    if k_rope.shape[0] != N or slots.numel() < N:
         raise ValueError("k_rope and slots must cover c_kv's tokens")
-    st = _lib_handle().kvk_paged_write(handle, layer, _ptr(c_kv), _DTYPE[c_kv.dtype],
-                                       _row_stride(c_kv), _ptr(k_rope), _row_stride(k_rope),
-                                       c_kv.shape[0], _ptr(slots), _stream(stream))
-    _check("kvk_paged_write", st)
+    st = _lib_handle().kvk_paged_write(handle, layer, c_kv.data_ptr(), _DTYPE[dtype],
+                                       _row_stride(c_kv), k_rope.data_ptr(), _row_stride(k_rope),
+                                       N, slots.data_ptr(), _raw_stream(stream, dev))
+    if st:
+        raise KvkError("kvk_paged_write", st)
 
 
 def kvk_mla_chunk(handle, layer, q_lat, q_rope, q_start, seq_lens, block_table, page_tokens,
@@ -405,36 +452,48 @@ def kvk_mla_chunk(handle, layer, q_lat, q_rope, q_start, seq_lens, block_table, 
     [N, H, d_rope] (same dtype, CUDA, last dim contiguous); q_start int32 [B + 1], seq_lens int32
     [B], block_table int32 [B, pages]; out [N, H, >=d] of the queries' dtype (last dim
     contiguous); lse fp32 [N, H] (optional); workspace uint8 CUDA tensor."""
-    _need_cuda(q_lat, "q_lat", tuple(_DTYPE))
-    _need_cuda(q_rope, "q_rope", (q_lat.dtype,))
-    _need_cuda(out, "out", (q_lat.dtype,))
-    _need_cuda(lse, "lse", (torch.float32,))
-    _need_cuda(workspace, "workspace")
-    for t, name in ((q_start, "q_start"), (seq_lens, "seq_lens"), (block_table, "block_table")):
-        _need_cuda(t, name, (torch.int32,))
-    if any(t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) for t in (q_lat, q_rope, out)):
-        raise ValueError("q_lat, q_rope and out must be [rows, heads, width] with contiguous width")
+    dtype, i32, dev = q_lat.dtype, torch.int32, _current_device(q_lat, "q_lat")
+    if not (q_lat.get_device() == dev and dtype in _DTYPE):
+        raise _bad(q_lat, "q_lat", tuple(_DTYPE), dev)
+    if not (q_rope.get_device() == dev and q_rope.dtype is dtype):
+        raise _bad(q_rope, "q_rope", (dtype,), dev)
+    if not (out.get_device() == dev and out.dtype is dtype):
+        raise _bad(out, "out", (dtype,), dev)
+    if lse is not None and not (lse.get_device() == dev and lse.dtype is torch.float32 and
+                                lse.is_contiguous()):
+        raise _bad(lse, "lse", (torch.float32,), dev)
+    if not (workspace.get_device() == dev and workspace.is_contiguous()):
+        raise _bad(workspace, "workspace", (), dev)
+    if not (q_start.get_device() == dev and q_start.dtype is i32 and q_start.is_contiguous()):
+        raise _bad(q_start, "q_start", _I32, dev)
+    if not (seq_lens.get_device() == dev and seq_lens.dtype is i32 and seq_lens.is_contiguous()):
+        raise _bad(seq_lens, "seq_lens", _I32, dev)
+    if not (block_table.get_device() == dev and block_table.dtype is i32):
+        raise _bad(block_table, "block_table", _I32, dev)
+    for t in (q_lat, q_rope, out):
+        if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+            raise ValueError("q_lat, q_rope and out must be [rows, heads, width] with contiguous "
+                             "width")
     if block_table.dim() != 2 or block_table.stride(1) != 1:
         raise ValueError("block_table must be [batch, pages] with contiguous rows")
-    if lse is not None and not lse.is_contiguous():
-        raise ValueError("lse must be contiguous")
-    N, H = q_lat.shape[0], q_lat.shape[1]
+    N, H, width = q_lat.shape
     B = seq_lens.numel()
+    rows, pages = block_table.shape
     if q_rope.shape[:2] != (N, H) or out.shape[:2] != (N, H) or q_start.numel() < B + 1 or \
-            block_table.shape[0] != B or not q_start.is_contiguous() or \
-            not seq_lens.is_contiguous() or (lse is not None and tuple(lse.shape) != (N, H)):
+            rows != B or (lse is not None and tuple(lse.shape) != (N, H)):
         raise ValueError("shapes of the queries, outputs, lengths and block table do not match")
-    info = kvk_get_layer_info(handle, layer)
-    if q_lat.shape[2] < info["d"] or out.shape[2] < info["d"] or q_rope.shape[2] < info["d_rope"]:
+    info = _layer_info(handle, layer)
+    if width < info.d or out.shape[2] < info.d or q_rope.shape[2] < info.d_rope:
         raise ValueError("q_lat, q_rope or out is narrower than the layer's rows")
     st = _lib_handle().kvk_mla_chunk(
-        handle, layer, _ptr(q_lat), _ptr(q_rope), _DTYPE[q_lat.dtype], _row_stride(q_lat),
+        handle, layer, q_lat.data_ptr(), q_rope.data_ptr(), _DTYPE[dtype], _row_stride(q_lat),
         _row_stride(q_lat, 1), _row_stride(q_rope), _row_stride(q_rope, 1), N, B, H,
-        _ptr(q_start), _ptr(seq_lens), _ptr(block_table), block_table.shape[1],
-        _row_stride(block_table), page_tokens, float(softmax_scale), _ptr(out), _row_stride(out),
-        _row_stride(out, 1), _ptr(lse), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream))
-    _check("kvk_mla_chunk", st)
+        q_start.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), pages,
+        block_table.stride(0) if B > 1 else pages, page_tokens, softmax_scale, out.data_ptr(),
+        _row_stride(out), _row_stride(out, 1), None if lse is None else lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
+    if st:
+        raise KvkError("kvk_mla_chunk", st)
 
 
 def kvk_chunk_workspace_bytes(handle, layer, n_q, batch, n_heads) -> int:
@@ -623,7 +682,7 @@ class Layout:
         out [N, H, d] of the queries' dtype."""
         N, H = q_lat.shape[0], q_lat.shape[1]
         if out is None:
-            out = torch.empty(N, H, self.layer_info(layer)["d"], dtype=q_lat.dtype,
+            out = torch.empty(N, H, _layer_info(self.handle, layer).d, dtype=q_lat.dtype,
                               device=q_lat.device)
         if workspace is None:
             workspace = self.new_chunk_workspace(layer, N, seq_lens.numel(), H)
