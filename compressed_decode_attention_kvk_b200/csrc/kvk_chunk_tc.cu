@@ -1491,13 +1491,13 @@ cudaError_t launch(const TcChunk& P, const CUtensorMap& hi, const CUtensorMap& l
                    cudaStream_t st) {
   auto k = chunk_tc_kernel<BITS, GROUP, kExp>;
   // the kernel hands registers from warpgroup to warpgroup: their number at launch is part of it
-  static const bool regs_ok = [&] {
+  static const bool ready = [&] {
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, k) == cudaSuccess && at.numRegs == (int)kLaunchRegs;
+    return cudaFuncGetAttributes(&at, k) == cudaSuccess && at.numRegs == (int)kLaunchRegs &&
+           cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) ==
+               cudaSuccess;
   }();
-  if (!regs_ok) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  if (!ready) return cudaErrorInvalidValue;
   k<<<dim3(2 * P.w.G), dim3(kThreads), smem, st>>>(P, hi, lo);
   return cudaGetLastError();
 }

@@ -452,6 +452,16 @@ def kvk_mla_chunk(handle, layer, q_lat, q_rope, q_start, seq_lens, block_table, 
     [N, H, d_rope] (same dtype, CUDA, last dim contiguous); q_start int32 [B + 1], seq_lens int32
     [B], block_table int32 [B, pages]; out [N, H, >=d] of the queries' dtype (last dim
     contiguous); lse fp32 [N, H] (optional); workspace uint8 CUDA tensor."""
+    if not q_lat.is_cuda:
+        raise ValueError("q_lat must be a CUDA tensor")
+    info = _layer_info(handle, layer)
+    _mla_chunk(handle, layer, info.d, info.d_rope, q_lat, q_rope, q_start, seq_lens, block_table,
+               page_tokens, softmax_scale, out, workspace, lse, stream)
+
+
+def _mla_chunk(handle, layer, d, d_rope, q_lat, q_rope, q_start, seq_lens, block_table, page_tokens,
+               softmax_scale, out, workspace, lse, stream):
+    """kvk_mla_chunk for a caller that knows the layer's widths."""
     dtype, i32, dev = q_lat.dtype, torch.int32, _current_device(q_lat, "q_lat")
     if not (q_lat.get_device() == dev and dtype in _DTYPE):
         raise _bad(q_lat, "q_lat", tuple(_DTYPE), dev)
@@ -482,8 +492,7 @@ def kvk_mla_chunk(handle, layer, q_lat, q_rope, q_start, seq_lens, block_table, 
     if q_rope.shape[:2] != (N, H) or out.shape[:2] != (N, H) or q_start.numel() < B + 1 or \
             rows != B or (lse is not None and tuple(lse.shape) != (N, H)):
         raise ValueError("shapes of the queries, outputs, lengths and block table do not match")
-    info = _layer_info(handle, layer)
-    if width < info.d or out.shape[2] < info.d or q_rope.shape[2] < info.d_rope:
+    if width < d or out.shape[2] < d or q_rope.shape[2] < d_rope:
         raise ValueError("q_lat, q_rope or out is narrower than the layer's rows")
     st = _lib_handle().kvk_mla_chunk(
         handle, layer, q_lat.data_ptr(), q_rope.data_ptr(), _DTYPE[dtype], _row_stride(q_lat),
@@ -681,13 +690,15 @@ class Layout:
         """Causal attention of packed query rows over the paged cache (kvk_mla_chunk); returns
         out [N, H, d] of the queries' dtype."""
         N, H = q_lat.shape[0], q_lat.shape[1]
+        if not 0 <= layer < len(self.anchor):
+            raise KvkError("kvk_mla_chunk", 1)
+        d = self.d[self.anchor[layer]]
         if out is None:
-            out = torch.empty(N, H, _layer_info(self.handle, layer).d, dtype=q_lat.dtype,
-                              device=q_lat.device)
+            out = torch.empty(N, H, d, dtype=q_lat.dtype, device=q_lat.device)
         if workspace is None:
             workspace = self.new_chunk_workspace(layer, N, seq_lens.numel(), H)
-        kvk_mla_chunk(self.handle, layer, q_lat, q_rope, q_start, seq_lens, block_table,
-                      page_tokens, softmax_scale, out, workspace, lse=lse, stream=stream)
+        _mla_chunk(self.handle, layer, d, self.d_rope, q_lat, q_rope, q_start, seq_lens,
+                   block_table, page_tokens, softmax_scale, out, workspace, lse, stream)
         return out
 
     def chunk_path_for(self, layer, dtype):

@@ -352,3 +352,52 @@ def test_chunk_takes_the_tensor_kernel(pkg):
     lay = pkg.Layout([0], [528], [8], 528, 64, 1, 64)
     assert lay.chunk_path_for(0, torch.bfloat16) == pkg.KVK_PATH_CUDA_CORE
     lay.close()
+
+
+@pytest.mark.parametrize("b", [2, 4, 8, 16])
+def test_write_codes_next_to_rounding_borders(pkg, oracle_mod, b):
+    """Values at and next to the borders (k + 1/2) s between two codes, where a quotient off by
+    one unit in its last place would round the other way."""
+    q = (1 << (b - 1)) - 1
+    rng = np.random.default_rng(b)
+    T, n = 512, 512
+    s = np.exp(rng.uniform(np.log(2e-4), np.log(200.0), T)).astype(np.float16)
+    k = rng.integers(-q, q, (T, n)).astype(np.float64)
+    v = ((k + 0.5) * s[:, None].astype(np.float64)).astype(np.float32)
+    v = (v.view(np.int32) + rng.integers(-3, 4, (T, n), dtype=np.int32)).view(np.float32)
+    # the largest: just below q s (which binary32 may round up at 16 bits), so that its quotient by
+    # q rounds up to the scale s exactly
+    v[:, 0] = np.nextafter(np.float32(q) * s.astype(np.float32), np.float32(0))
+    v = np.clip(v, -v[:, :1], v[:, :1])
+    c = torch.from_numpy(v)
+    kr = torch.zeros(T, 0)
+    rows, sc, _ = oracle_mod.quantize_rows(v, np.zeros((T, 0), np.float32), n, b)
+    assert np.array_equal(sc.view(np.uint16).reshape(-1), s.view(np.uint16))
+    lay = pkg.Layout([0], [n], [b], n, 0, 1, T)
+    try:
+        lay.paged_write(0, c.cuda(), kr.cuda(), i32(list(range(T))))
+        codes, _ = lay.cache_views(0)
+        assert np.array_equal(codes[0].cpu().numpy()[:, :rows.shape[1]], rows)
+    finally:
+        lay.close()
+
+
+def test_write_long_rows(pkg, oracle_mod):
+    """Rows beyond the short form's 640 elements."""
+    d, dR, T = 1024, 64, 9
+    g = torch.Generator().manual_seed(3)
+    c, kr = _values(g, T, d, dR)
+    for b, G in [(8, 0), (4, 32), (0, 0)]:
+        lay = pkg.Layout([0], [d], [b], d, dR, 1, 16, scale_group=G)
+        try:
+            slots = [3, 1, 15, 0, 7, -1, 9, 8, 4]
+            lay.paged_write(0, c.cuda(), kr.cuda(), i32(slots))
+            codes, scales = lay.cache_views(0)
+            rows, s = _row_refs(oracle_mod, c, kr, d, b, G)
+            keep = [i for i in range(T) if slots[i] >= 0]
+            at = [slots[i] for i in keep]
+            assert np.array_equal(codes[0].cpu().numpy()[at], rows[keep])
+            assert np.array_equal(scales[0].reshape(16, -1).cpu().view(torch.int16).numpy()
+                                  .view(np.uint16)[at], s[keep])
+        finally:
+            lay.close()
