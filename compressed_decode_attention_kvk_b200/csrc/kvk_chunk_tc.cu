@@ -10,7 +10,7 @@
 // shared memory: 64 cycles per MMA at N = 256 (the full rate; one CTA alone reaches it only with
 // 128 rows, and takes 80 cycles for 64 rows with .ws), 46 at N = 128 (ideal 32).
 //
-// Work.  A row tile costs its 128-token blocks plus kPieceCost (query staging, output); every
+// Work.  A row tile costs its 128-token blocks plus kCost (query staging, output); every
 // cluster takes an equal slice of the batch's cost.  A tile that falls into several slices is
 // written as partials (running reference m, weight sum l, un-normalised o) and joined by
 // chunk_merge_kernel; a cluster owns at most two partial tiles, its first and its last, so the
@@ -67,7 +67,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kKWarp0 = 4, kVWarp0 = 8, kMmaWarp = 12, kTokWarp = 13, kRelayWarp = 14, kLoadWarp = 15;   // (see below)
 constexpr uint32_t kAtom = 8192;       // 64 rows x 128 bytes
-constexpr int kTokStages = 3;
+constexpr int kMinTok = 3, kMaxTok = 6;   // token stages: as many as the memory left holds
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;        // S buffers at 256 and 320 (64 columns); O at 0
 constexpr float kLog2e = 1.4426950408889634f;
@@ -99,10 +99,9 @@ struct alignas(16) TokStage {
 constexpr int kEnd = 1, kFirst = 2, kLast = 4;
 
 struct Shared {
-  TokStage tok[kTokStages];
   int8_t qexp[4][64];                  // per row: e of its query's scaling 2^e
   float xch[2][256];                   // maxima (at a piece's end: sums) of a row's threads
-  uint64_t tok_full[kTokStages], tok_empty[kTokStages];
+  uint64_t tok_full[kMaxTok], tok_empty[kMaxTok];
   // operands: written (by this CTA's warps), passed on (to the leader, by both relays), free
   uint64_t k_full[kMaxK], k_ready[kMaxK], k_empty[kMaxK];
   uint64_t v_full[4], v_ready[4], v_empty[4];
@@ -114,7 +113,20 @@ struct Shared {
   uint32_t tmem_base, abort_word;
 };
 
-static_assert(sizeof(Shared) <= 11264, "leaves 27 atoms of 8 KB");
+static_assert(sizeof(Shared) + kMinTok * sizeof(TokStage) <= 11264, "leaves 27 atoms of 8 KB");
+
+// Position in the ring of token stages.
+struct TokRing {
+  int n, st = 0;
+  uint32_t par = 0;
+  __device__ __forceinline__ explicit TokRing(int stages) : n(stages) {}
+  __device__ __forceinline__ void next() {
+    if (++st == n) {
+      st = 0;
+      par ^= 1;
+    }
+  }
+};
 
 // The fields of a piece's first block that query staging reads.
 struct QueryTile {
@@ -125,8 +137,8 @@ struct TcChunk {
   ChunkArgs a;
   ChunkWork w;
   int NL, NA, NV;          // latent atoms (padded to whole 128), all atoms, V atoms per CTA
-  int NK, NVS;             // K ring slots, V stages
-  uint32_t off_k, off_v, off_p, off_misc;
+  int NK, NVS, NT;         // K ring slots, V stages, token stages
+  uint32_t off_k, off_v, off_p, off_misc, off_tok;
   uint32_t idesc_s, idesc_o2, idesc_o1;   // score; output with 128 / 64 features per CTA
   int q_bf16;
   // expanded rows (kExp)
@@ -449,12 +461,17 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
   constexpr bool kTok = !GROUP && !kBf16;             // one scale per token
   constexpr bool kLo = kSplit<BITS, GROUP>;
   constexpr int kSoftWarps = kExp ? 8 : 4;
+  // cost of a row tile beside its blocks, in blocks (a ragged batch of 16 over expanded rows: 951 us
+  // with 2, 831 with 4, 822 with 6; decode of 32 sequences from packed rows: 230, 245, 250)
+  constexpr int kCost = kExp ? 5 : 2;
   constexpr int kStep = 2;                            // atoms of a K ring slot
   // the output MMAs' warp is the one that has no other work: the relay's with expanded rows, else
   // the loads'
   constexpr int kOutWarp = kExp ? kRelayWarp : kLoadWarp;
   extern __shared__ __align__(1024) uint8_t smem[];
   const ChunkArgs& a = P.a;
+  TokStage* const toks = reinterpret_cast<TokStage*>(smem + P.off_tok);
+  TokRing ring(P.NT);
   Shared& S = *reinterpret_cast<Shared*>(smem + P.off_misc);
   const uint32_t q_s = smem_u32(smem), k_s = q_s + P.off_k, v_s = q_s + P.off_v, p_s = q_s + P.off_p;
   // The warp index, and what a warp reads from shared memory to steer its MMAs, go through a
@@ -468,7 +485,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
 
   if (tid == 0) {
     S.abort_word = 0;
-    for (int i = 0; i < kTokStages; ++i) {
+    for (int i = 0; i < kMaxTok; ++i) {
       mbar_init(&S.tok_full[i], 1);
       // softmax warps, loading or converting warps and relay, the leader's MMA warps
       mbar_init(&S.tok_empty[i], kSoftWarps + (kExp ? 5 : 9) + (rank == 0 ? 2 : 0));
@@ -568,7 +585,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
           loaded = seq;
         }
         const int k = f - pre[seq];
-        const int c = kPieceCost + blocks_of(s.len, s.count, a.H, k * 128, s.count * a.H);
+        const int c = kCost + blocks_of(s.len, s.count, a.H, k * 128, s.count * a.H);
         if (pass == 0) {
           cost += c;
         } else {
@@ -625,10 +642,11 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       uint32_t kpar = 0;
       bool ok = true;
       for (int g = 0;; ++g) {
-        const int st = g % kTokStages;
-        ok = all(&S.tok_full[st], (g / kTokStages) & 1);
+        const int st = ring.st;
+        ok = all(&S.tok_full[st], ring.par);
+        ring.next();
         if (!ok) break;
-        const int now = uniform(*const_cast<volatile int32_t*>(&S.tok[st].flags));
+        const int now = uniform(*const_cast<volatile int32_t*>(&toks[st].flags));
         if (lane == 0) mbar_arrive(&S.tok_empty[st]);
         if (now & kEnd) break;
         if (scores) {
@@ -701,18 +719,19 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       while (ok && base < u1) {
         const int rows = s.count * a.H;
         const int nblk = blocks_of(s.len, s.count, a.H, k * 128, rows);
-        const int64_t x0 = u0 - base - kPieceCost, x1 = u1 - base - kPieceCost;
+        const int64_t x0 = u0 - base - kCost, x1 = u1 - base - kCost;
         const int b0 = (int)max((int64_t)0, min(x0, (int64_t)nblk));
         const int b1 = (int)max((int64_t)0, min(x1, (int64_t)nblk));
 #pragma unroll 1
         for (int blk = b0; ok && blk < b1; ++blk, ++g) {
-          const int st = g % kTokStages;
-          ok = wait(&S.tok_empty[st], ((g / kTokStages) & 1) ^ 1);
+          const int st = ring.st;
+          ok = wait(&S.tok_empty[st], ring.par ^ 1);
+          ring.next();
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
           }
-          TokStage& T = S.tok[st];
+          TokStage& T = toks[st];
           const int t0 = blk << 7;
           int sl[4];
 #pragma unroll
@@ -774,7 +793,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
           if (lane == 0) mbar_arrive(&S.tok_full[st]);
         }
         if (b1 > b0) ++piece;
-        base += kPieceCost + nblk;
+        base += kCost + nblk;
         ++k;
         if (base < u1 && k * 128 >= rows) {   // the next sequence that has query rows
           k = 0;
@@ -795,10 +814,10 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       }
     }
     if (ok) {
-      const int st = g % kTokStages;
-      ok = __all_sync(0xffffffffu, wait(&S.tok_empty[st], ((g / kTokStages) & 1) ^ 1));
+      const int st = ring.st;
+      ok = __all_sync(0xffffffffu, wait(&S.tok_empty[st], ring.par ^ 1));
       if (ok && lane == 0) {
-        S.tok[st].flags = kEnd;
+        toks[st].flags = kEnd;
         mbar_arrive(&S.tok_full[st]);
       }
     }
@@ -827,9 +846,10 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         bool moved = false;
         if (gk < end) {
           if (ik < 0) {
-            const int st = gk % kTokStages;
-            if (mbar_test(&S.tok_full[st], (gk / kTokStages) & 1)) {
-              const int fl = *const_cast<volatile int32_t*>(&S.tok[st].flags);
+            const int st = ring.st;
+            if (mbar_test(&S.tok_full[st], ring.par)) {
+              ring.next();
+              const int fl = *const_cast<volatile int32_t*>(&toks[st].flags);
               mbar_arrive(&S.tok_empty[st]);
               moved = true;
               if (fl & kEnd) end = gk;
@@ -882,15 +902,16 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     int kslot = 0;
     uint32_t kpar = 1;
     bool ok = kExp;
-    for (int g = 0; ok; ++g) {
-      const int st = g % kTokStages;
-      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], (g / kTokStages) & 1));
-      if (!ok || (S.tok[st].flags & kEnd)) break;
+    while (ok) {
+      const int st = ring.st;
+      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], ring.par));
+      ring.next();
+      if (!ok || (toks[st].flags & kEnd)) break;
       // a lane per box: slots of the block's boxes, atoms of the step
       const int per = 64 / P.box, lg = 31 - __clz(per);
       int sl = P.pool_slots;                          // reads as zero
       if (lane < 2 * per) {
-        const int x = S.tok[st].slot[64 * (int)rank + (lane & (per - 1)) * P.box];
+        const int x = toks[st].slot[64 * (int)rank + (lane & (per - 1)) * P.box];
         if (x >= 0) sl = x;
       }
       __syncwarp();
@@ -924,10 +945,11 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     uint32_t armed = 0, landing = 0;                  // barriers used so far, and their last phase
     bool ok = true;
     for (int g = 0;; ++g) {
-      const int st = g % kTokStages;
-      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], (g / kTokStages) & 1));
+      const int st = ring.st;
+      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], ring.par));
+      ring.next();
       if (!ok) break;
-      const TokStage& T = S.tok[st];
+      const TokStage& T = toks[st];
       const int fl = T.flags;
       if (fl & kEnd) break;
       if (fl & kFirst) {
@@ -984,10 +1006,11 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     const int vw = warp - kVWarp0;
     bool ok = true;
     for (int g = 0;; ++g) {
-      const int st = g % kTokStages;
-      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], (g / kTokStages) & 1));
+      const int st = ring.st;
+      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], ring.par));
+      ring.next();
       if (!ok) break;
-      const TokStage& T = S.tok[st];
+      const TokStage& T = toks[st];
       const int fl = T.flags;
       if (fl & kEnd) break;
       Row<GROUP> row[4];
@@ -1056,14 +1079,14 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
     int kslot = 0;
     uint32_t kpar = 1;
     bool ok = true, last = false;
-    int g = 0;             // next block to be taken from the token ring
     Row<GROUP> row[2];     // of the block whose rows are loaded next
     Unit<BITS, GROUP> cur[kPer][2], nxt[kPer][2];
     bool real[2], next_real[2];
     auto take = [&]() -> bool {
-      const int s1 = g % kTokStages;
-      if (!__all_sync(0xffffffffu, wait(&S.tok_full[s1], (g / kTokStages) & 1))) return false;
-      const TokStage& T = S.tok[s1];
+      const int s1 = ring.st;
+      if (!__all_sync(0xffffffffu, wait(&S.tok_full[s1], ring.par))) return false;
+      ring.next();
+      const TokStage& T = toks[s1];
       last = (T.flags & kLast) != 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -1072,7 +1095,6 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.tok_empty[s1]);
-      ++g;
       return true;
     };
     auto load = [&](int step, Unit<BITS, GROUP> (&to)[kPer][2]) {
@@ -1087,11 +1109,11 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       }
     };
     for (;;) {             // one piece
-      const int st = g % kTokStages;
-      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], (g / kTokStages) & 1));
+      const int st = ring.st;
+      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], ring.par));
       if (!ok) break;
-      if (S.tok[st].flags & kEnd) break;
-      const QueryTile head = {S.tok[st].row0, S.tok[st].flat0, S.tok[st].rows, S.tok[st].piece};
+      if (toks[st].flags & kEnd) break;
+      const QueryTile head = {toks[st].row0, toks[st].flat0, toks[st].rows, toks[st].piece};
       ok = take();
       if (!ok) break;
       load(0, cur);
@@ -1172,10 +1194,11 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       return __all_sync(0xffffffffu, wait(&S.x_bar, met++ & 1));
     };
     for (int g = 0;; ++g) {
-      const int st = g % kTokStages;
-      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], (g / kTokStages) & 1));
+      const int st = ring.st;
+      ok = __all_sync(0xffffffffu, wait(&S.tok_full[st], ring.par));
+      ring.next();
       if (!ok) break;
-      const TokStage& T = S.tok[st];
+      const TokStage& T = toks[st];
       const int fl = T.flags;
       if (fl & kEnd) break;
       if (fl & kFirst) {
@@ -1520,20 +1543,22 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkWork& w, int dtype, c
   P.NA = row_atoms(a.d, a.d_rope);
   P.NV = P.NL / 2;
   P.NVS = P.NV <= 2 ? 2 : 1;
-  const int room = (int)((kSmemLimit - (int)sizeof(Shared)) / (int)kAtom) - P.NA - 2 * P.NV * P.NVS - 2;
+  const int room = (kSmemLimit - (int)(sizeof(Shared) + kMinTok * sizeof(TokStage))) / (int)kAtom - P.NA - 2 * P.NV * P.NVS - 2;
   P.NK = std::min(kMaxK, room / 2);   // slots of two atoms
   P.off_k = (uint32_t)P.NA * kAtom;
   P.off_v = P.off_k + (uint32_t)(2 * P.NK) * kAtom;
   P.off_p = P.off_v + (uint32_t)(2 * P.NV * P.NVS) * kAtom;
   P.off_misc = P.off_p + 2 * kAtom;
+  P.off_tok = (uint32_t)align_up_sz(P.off_misc + sizeof(Shared), 16);
+  P.NT = std::min(kMaxTok, (kSmemLimit - (int)P.off_tok) / (int)sizeof(TokStage));
   const bool bf = a.b == KVK_BITS_BF16;
   P.idesc_s = idesc_of(bf, 128, false);
   P.idesc_o2 = idesc_of(bf, 256, true);
   P.idesc_o1 = idesc_of(bf, 128, true);
   P.q_bf16 = dtype == KVK_BF16;
-  const size_t smem = P.off_misc + sizeof(Shared);
+  const size_t smem = P.off_tok + (size_t)P.NT * sizeof(TokStage);
   // the prologue's prefix sums use the rings' memory
-  if (w.G >= 32 * kMergeRounds || P.NK < 2 || smem > (size_t)kSmemLimit || (size_t)(a.batch + 1) * 4 > P.off_misc)
+  if (w.G >= 32 * kMergeRounds || P.NT < kMinTok || P.NK < 2 || smem > (size_t)kSmemLimit || (size_t)(a.batch + 1) * 4 > P.off_misc)
     return cudaErrorInvalidValue;
   CUtensorMap hi, lo;
   memset(&hi, 0, sizeof(hi));

@@ -5,8 +5,6 @@
 
 namespace kvk {
 
-constexpr int kPieceCost = 2;   // cost of a row tile beside its 128-token blocks
-
 // Header of one partial row tile (two per cluster: the tile its slice starts within, and the one
 // that it starts but does not finish).
 struct ChunkPartial {
