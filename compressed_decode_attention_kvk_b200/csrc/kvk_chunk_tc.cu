@@ -722,6 +722,36 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         const int64_t x0 = u0 - base - kCost, x1 = u1 - base - kCost;
         const int b0 = (int)max((int64_t)0, min(x0, (int64_t)nblk));
         const int b1 = (int)max((int64_t)0, min(x1, (int64_t)nblk));
+        auto slots_of = [&](int t0, int (&sl)[4]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = t0 + 32 * i + lane;
+            sl[i] = t < s.len ? chunk_slot(a, seq, t) : -1;
+          }
+        };
+        // scales and marks; the rows that this CTA converts for the scores are fetched into L2
+        auto scales_of = [&](const int (&sl)[4], float (&sc)[4], float (&mk)[4]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sc[i] = (kTok && sl[i] >= 0) ? __half2float(a.scales[sl[i]]) : 1.0f;
+            mk[i] = (kExp && sl[i] >= 0) ? __ldg(P.mark + sl[i]) : 0.0f;
+          }
+#pragma unroll
+          for (int i = 0; !kExp && i < 2; ++i) {
+            const int my = rank ? sl[2 + i] : sl[i];
+            if (my >= 0) {
+              const uint8_t* p = a.codes + (int64_t)my * a.row_bytes;
+#pragma unroll 1
+              for (int x = 0; x < a.row_bytes; x += 128) prefetch_l2(p + x);
+            }
+          }
+        };
+        int sl[4];
+        float sc[4], mk[4];
+        if (b0 < b1) {
+          slots_of(b0 << 7, sl);
+          scales_of(sl, sc, mk);
+        }
 #pragma unroll 1
         for (int blk = b0; ok && blk < b1; ++blk, ++g) {
           const int st = ring.st;
@@ -733,28 +763,9 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
           }
           TokStage& T = toks[st];
           const int t0 = blk << 7;
-          int sl[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t = t0 + 32 * i + lane;
-            sl[i] = t < s.len ? chunk_slot(a, seq, t) : -1;
-          }
-          // the rows that this CTA converts for the scores are fetched into L2 now
-#pragma unroll
-          for (int i = 0; !kExp && i < 2; ++i) {
-            const int my = rank ? sl[2 + i] : sl[i];
-            if (my >= 0)
-              asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                               a.codes + (int64_t)my * a.row_bytes),
-                           "r"(a.row_bytes)
-                           : "memory");
-          }
-          float sc[4], mk[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mk[i] = (kExp && sl[i] >= 0) ? __ldg(P.mark + sl[i]) : 0.0f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sc[i] = (kTok && sl[i] >= 0) ? __half2float(a.scales[sl[i]]) : 1.0f;
+          // the next block's slots are on their way while this one's entries are written
+          int sn[4];
+          if (blk + 1 < b1) slots_of(t0 + 128, sn);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             T.slot[32 * i + lane] = sl[i];
@@ -791,6 +802,11 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&S.tok_full[st]);
+          if (blk + 1 < b1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sl[i] = sn[i];
+            scales_of(sl, sc, mk);
+          }
         }
         if (b1 > b0) ++piece;
         base += kCost + nblk;
@@ -1219,38 +1235,43 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       ok = __all_sync(0xffffffffu, wait(&S.s_full[g & 1], (g >> 1) & 1));
       if (!ok) break;
       tc_fence_after();
-      float s[kCols];
+      // w_t = z_t + log2 s_t of 32 columns from c0 on (the S columns are read again for the second
+      // pass: the loops over a thread's columns stay rolled, since the steady loops of all roles
+      // share an instruction cache that they overfill)
       const uint32_t sb = tmem + kSCol + 64u * (g & 1) + (uint32_t)(kCols * cg) + lanes;
-#pragma unroll
-      for (int i = 0; i < kCols; i += 32) tmem_ld32(sb + i, s + i);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_at(&S.s_free[g & 1], 0);
-      // w_t = z_t + log2 s_t, and its maximum over this half
-      const float4* lsc4 = reinterpret_cast<const float4*>(T.lsc + col0);
-      const float4* sc4 = reinterpret_cast<const float4*>(T.sc + col0);
       const int vis = lim - T.t0 - col0;             // columns that the row sees
-      float mx = -CUDART_INF_F;
+      const bool partly = __any_sync(0xffffffffu, vis < kCols);
+      auto weights = [&](int c0, float (&w)[32]) {
+        tmem_ld32(sb + c0, w);
+        tmem_wait_ld();
+        const float4* lsc4 = reinterpret_cast<const float4*>(T.lsc + col0 + c0);
+        const float4* sc4 = reinterpret_cast<const float4*>(T.sc + col0 + c0);
 #pragma unroll
-      for (int i = 0; i < kCols / 4; ++i) {
-        const float4 b = lsc4[i];
-        float4 c = make_float4(1.f, 1.f, 1.f, 1.f);
-        if constexpr (kTok) c = sc4[i];
-        const float bb[4] = {b.x, b.y, b.z, b.w}, cc[4] = {c.x, c.y, c.z, c.w};
+        for (int i = 0; i < 8; ++i) {
+          const float4 b = lsc4[i];
+          float4 c = make_float4(1.f, 1.f, 1.f, 1.f);
+          if constexpr (kTok) c = sc4[i];
+          const float bb[4] = {b.x, b.y, b.z, b.w}, cc[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float z = s[4 * i + k];
-          if constexpr (kTok) z *= cc[k];
-          s[4 * i + k] = fmaf(z, rc, bb[k]);
+          for (int k = 0; k < 4; ++k) {
+            float z = w[4 * i + k];
+            if constexpr (kTok) z *= cc[k];
+            w[4 * i + k] = fmaf(z, rc, bb[k]);
+          }
         }
-      }
-      if (__any_sync(0xffffffffu, vis < kCols)) {
+        if (partly) {
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) s[i] = i < vis ? s[i] : -CUDART_INF_F;
-      }
+          for (int i = 0; i < 32; ++i) w[i] = c0 + i < vis ? w[i] : -CUDART_INF_F;
+        }
+      };
+      float s[32];
+      float mx = -CUDART_INF_F;
+#pragma unroll 1
+      for (int c0 = 0; c0 < kCols; c0 += 32) {
+        weights(c0, s);
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) mx = fmaxf(mx, s[i]);
+        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, s[i]);
+      }
       S.xch[g & 1][tid] = mx;
       ok = meet();
       if (!ok) break;
@@ -1264,53 +1285,52 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         m = mx;
       }
       const float mref = m == -CUDART_INF_F ? 0.0f : m;
-      uint32_t pk[kCols / 2];
-      const float4* isc4 = reinterpret_cast<const float4*>(T.isc + col0);
-      float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kCols / 4; ++i) {
-        float4 c = make_float4(1.f, 1.f, 1.f, 1.f);
-        if constexpr (kTok) c = isc4[i];
-        const float cc[4] = {c.x, c.y, c.z, c.w};
-        float e[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          e[k] = ex2_approx(s[4 * i + k] - mref);
-          if (k & 1) l1 = fmaf(e[k], cc[k], l1); else l0 = fmaf(e[k], cc[k], l0);
+#pragma unroll 1
+      for (int c0 = 0; c0 < kCols; c0 += 32) {
+        if (kCols > 32) weights(c0, s);
+        if (c0 + 32 == kCols) {                       // S has been read for the last time
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_at(&S.s_free[g & 1], 0);
         }
-        if constexpr (kBf16) {
-          const __nv_bfloat162 x = __floats2bfloat162_rn(e[0], e[1]);
-          const __nv_bfloat162 y = __floats2bfloat162_rn(e[2], e[3]);
-          pk[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
-          pk[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
-        } else {
-          const __half2 x = __floats2half2_rn(e[0], e[1]);
-          const __half2 y = __floats2half2_rn(e[2], e[3]);
-          pk[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
-          pk[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
+        const float4* isc4 = reinterpret_cast<const float4*>(T.isc + col0 + c0);
+        uint32_t pk[16];
+        float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float4 c = make_float4(1.f, 1.f, 1.f, 1.f);
+          if constexpr (kTok) c = isc4[i];
+          const float cc[4] = {c.x, c.y, c.z, c.w};
+          float e[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            e[k] = ex2_approx(s[4 * i + k] - mref);
+            if (k & 1) l1 = fmaf(e[k], cc[k], l1); else l0 = fmaf(e[k], cc[k], l0);
+          }
+          pk[2 * i] = pack_out(kBf16, e[0], e[1]);
+          pk[2 * i + 1] = pack_out(kBf16, e[2], e[3]);
         }
+        l += l0 + l1;
+        if (c0 == 0 && g > 0) {                       // the previous output MMA has read P, left O
+          ok = __all_sync(0xffffffffu, wait(&S.pv_done, (g - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t row = p_s + (uint32_t)hh * kAtom + (uint32_t)r * 128u;
+        const int c1 = (kCols * cg + c0) >> 3;        // first 16-byte chunk of the row
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          sts128(row + (uint32_t)(((c + c1) ^ (r & 7)) << 4),
+                 make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]));
       }
-      l += l0 + l1;
+      if (!ok) break;
       // the scales and this block's header have been read
       const int last = fl & kLast, dest = T.dest, t_seq = T.seq, t_b1 = T.b1, t_nblk = T.nblk;
       const int t_flat0 = T.flat0, t_row0 = T.row0, t_rows = T.rows;
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.tok_empty[st]);
-      // the previous output MMA has read P and left O
-      if (g > 0) {
-        ok = __all_sync(0xffffffffu, wait(&S.pv_done, (g - 1) & 1));
-        if (!ok) break;
-        tc_fence_after();
-      }
       if (!(fl & kFirst) && __any_sync(0xffffffffu, alpha != 1.0f)) {
         rescale_o(obase, ocg, alpha);
-      }
-      {
-        const uint32_t row = p_s + (uint32_t)hh * kAtom + (uint32_t)r * 128u;
-#pragma unroll
-        for (int c = 0; c < kCols / 8; ++c)
-          sts128(row + (uint32_t)(((c + kCols / 8 * cg) ^ (r & 7)) << 4),
-                 make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]));
       }
       if constexpr (kExp) fence_proxy_async_smem();
       tc_fence_before();

@@ -45,10 +45,13 @@ int chunk_path(const kvk_layout* L, const AnchorDesc& A, int dtype) {
 }
 
 // Whether a call's rows are converted once ahead of the attention (kvk_chunk_expand.cu) instead
-// of in every row tile: from kExpandTiles row tiles per sequence on, over the batch.
-constexpr int kExpandTiles = 3;
-bool expand_pays(int n_q, int batch, int n_heads) {
-  return (int64_t)n_q * n_heads >= (int64_t)kExpandTiles * 128 * batch;
+// of in every row tile: from two row tiles of 128 per sequence on, over the batch, or one where the
+// rows are bf16 and nothing is converted but much is loaded.  8 sequences of 4096 tokens, 40 heads,
+// d = 512, row tiles per sequence (us converting / expanded): 8 bits 1.9 (71 / 76), 2.5 (86 / 83);
+// 16 bits 1.9 (87 / 93), 2.5 (109 / 107); bf16 0.6 (61 / 59), 1.2 (89 / 64).
+bool expand_pays(int b, int n_q, int batch, int n_heads) {
+  const int tiles = b == KVK_BITS_BF16 ? 1 : 2;
+  return (int64_t)n_q * n_heads >= (int64_t)tiles * 128 * batch;
 }
 
 size_t chunk_bytes(const kvk_layout* L, const AnchorDesc& A, bool expand, void* base,
@@ -152,7 +155,7 @@ kvk_status kvk_chunk_workspace_bytes(const kvk_layout* L, int layer, int n_q, in
       batch > kvk::kMaxPagedBatch || n_heads < 1 || n_heads > 4096)
     return KVK_ERR_INVALID_ARG;
   const AnchorDesc& A = L->anchors[L->slot[layer]];
-  *bytes = chunk_bytes(L, A, expand_pays(n_q, batch, n_heads), nullptr, nullptr);
+  *bytes = chunk_bytes(L, A, expand_pays(A.b, n_q, batch, n_heads), nullptr, nullptr);
   return KVK_OK;
 }
 
@@ -231,7 +234,7 @@ kvk_status kvk_mla_chunk(kvk_layout* L, int layer, const void* q_lat, const void
     kvk::ChunkWork w;
     memset(&w, 0, sizeof(w));
     // a box of expanded rows is 8 rows at least (the swizzle's period) and lies in one page
-    const bool expand = expand_pays(n_q, batch, n_heads) && page_tokens >= 8 &&
+    const bool expand = expand_pays(A.b, n_q, batch, n_heads) && page_tokens >= 8 &&
                         workspace_bytes >= chunk_bytes(L, A, true, nullptr, nullptr);
     if (workspace_bytes < chunk_bytes(L, A, expand, workspace, &w)) return KVK_ERR_WORKSPACE;
     e = kvk::launch_chunk_tc(a, w, dtype, st);
