@@ -15,6 +15,8 @@
 // cached tokens the kernel takes 8.1 us with S = 8 and 44.8 us with S = 1.
 #include <float.h>
 
+#include <math_constants.h>
+
 #include "kvk_paged.cuh"
 
 namespace kvk {
@@ -137,14 +139,22 @@ __global__ void __launch_bounds__(kHG * 32) chunk_fma_kernel(const __grid_consta
   const int row = blockIdx.x, h = blockIdx.y * kHG + warp;
   const bool hv = h < a.H;
 
-  // the sequence of this query row: the first whose rows end behind it
+  // the sequence of this query row: the first whose rows end behind it.  Every CTA checks all
+  // offsets (they are read for the search anyway): where any is wrong, the call writes nothing.
   int seq = 0;
+  bool bad = false;
   for (int i0 = 0; i0 < a.batch; i0 += nt) {
-    const bool before = i0 + tid < a.batch && __ldg(a.q_start + i0 + tid + 1) <= row;
+    const int i = i0 + tid;
+    bool before = false;
+    if (i < a.batch) {
+      const int s0 = __ldg(a.q_start + i), s1 = __ldg(a.q_start + i + 1);
+      bad = bad || s0 < 0 || s1 < s0 || s1 > a.n_q;
+      before = s1 <= row;
+    }
     seq += __syncthreads_count(before);
   }
-  bool bad = false;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {   // one CTA reports what had to be clamped
+  const bool stop = __syncthreads_or(bad) != 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {   // one CTA reports
     for (int i = tid; i < a.batch; i += nt) {
       bool b1;
       chunk_seq(a, i, &b1);
@@ -152,6 +162,7 @@ __global__ void __launch_bounds__(kHG * 32) chunk_fma_kernel(const __grid_consta
     }
     if (bad) atomicOr(a.flags, KVK_FLAG_SEQ_LEN);
   }
+  if (stop) return;
   if (seq >= a.batch) return;                  // a row behind the last sequence: left alone
   const ChunkSeq s = chunk_seq(a, seq, &bad);
   if (row < s.row0 || row >= s.row0 + s.count) return;
@@ -195,6 +206,9 @@ __global__ void __launch_bounds__(kHG * 32) chunk_fma_kernel(const __grid_consta
       const float* cr = cs + lane * ldc;
       for (int k = 0; k < n; ++k) acc = fmaf(qr[k], cr[k], acc);
       z2 = acc * ss[lane] * zscale;
+      // an element that is not finite leaves no finite score (finite x inf, 0 x inf, inf - inf);
+      // as NaN it turns the whole row into NaN, a -inf included, as the tensor-core kernel does
+      if (!isfinite(z2)) z2 = CUDART_NAN_F;
     }
     const float mn = fmaxf(m, warp_max(z2));
     const float alpha = (m == -INFINITY || mn == -INFINITY) ? 0.0f : exp2f(m - mn);

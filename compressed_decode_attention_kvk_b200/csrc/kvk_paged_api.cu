@@ -83,10 +83,28 @@ kvk_status kvk_paged_plan(kvk_layout* L, const int32_t* dev_cached, const int32_
       !dev_q_start || !dev_free_count_out || (free_capacity > 0 && !dev_free_pages) ||
       (max_new > 0 && !dev_slots))
     return KVK_ERR_INVALID_ARG;
-  // the lengths are read while the results are written
-  if (dev_seq_lens == dev_cached || dev_seq_lens == dev_new || dev_q_start == dev_cached ||
-      dev_q_start == dev_new)
-    return KVK_ERR_INVALID_ARG;
+  // the inputs are read while the results are written: no result overlaps an input or another
+  // result (but the free count may be updated in place)
+  struct Span {
+    const int32_t* p;
+    int64_t n;
+  };
+  const Span in[] = {{dev_cached, batch}, {dev_new, batch}, {dev_free_pages, free_capacity},
+                     {dev_free_count, 1}};
+  const Span res[] = {{dev_block_table, (batch - 1) * table_stride + table_pages},
+                      {dev_seq_lens, batch}, {dev_q_start, batch + 1}, {dev_slots, max_new},
+                      {dev_positions, dev_positions ? max_new : 0}, {dev_free_count_out, 1}};
+  auto meet = [](const Span& x, const Span& y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    return x.n > 0 && y.n > 0 && a < b + 4 * (uintptr_t)y.n && b < a + 4 * (uintptr_t)x.n;
+  };
+  for (int i = 0; i < 6; ++i) {
+    for (int j = i + 1; j < 6; ++j)
+      if (meet(res[i], res[j])) return KVK_ERR_INVALID_ARG;
+    for (const Span& x : in)
+      if (meet(res[i], x) && !(i == 5 && x.p == dev_free_count && x.p == res[5].p))
+        return KVK_ERR_INVALID_ARG;
+  }
   for (const void* p : {(const void*)dev_cached, (const void*)dev_new, (const void*)dev_free_pages,
                         (const void*)dev_free_count, (const void*)dev_block_table,
                         (const void*)dev_seq_lens, (const void*)dev_q_start,
@@ -170,7 +188,7 @@ kvk_status kvk_mla_chunk(kvk_layout* L, int layer, const void* q_lat, const void
   if (!L || layer < 0 || layer >= L->n_layers || !L->arena) return KVK_ERR_INVALID_ARG;
   if (!known_dtype(dtype)) return KVK_ERR_INVALID_ARG;
   if (n_q < 0 || batch < 1 || batch > kvk::kMaxPagedBatch || n_heads < 1 || n_heads > 4096 ||
-      (int64_t)n_q * n_heads >= (int64_t)1 << 31)
+      (int64_t)n_q * n_heads > ((int64_t)1 << 31) - 256)   // row indexes of whole tiles are ints
     return KVK_ERR_INVALID_ARG;
   const int shift = page_shift(page_tokens);
   if (shift < 0 || table_pages < 1 || table_stride < table_pages) return KVK_ERR_INVALID_ARG;

@@ -383,6 +383,14 @@ def _raw_stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
+def _on(stream):
+    """Tensors that a call allocates itself belong to the stream it runs on: the allocator would
+    otherwise hand them to (or take them from) work of the current stream too early."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream.cuda_stream))
+
+
 _I32 = (torch.int32,)
 _KV_TYPES = (torch.float32, torch.bfloat16)
 
@@ -669,7 +677,8 @@ class Layout:
         place, free_pages[:free_count] is the free list, max_new bounds the new tokens of the
         batch.  Returns a PagedPlan (out, if one is given)."""
         if out is None:
-            out = self.new_paged_plan(cached.numel(), max_new)
+            with _on(stream):
+                out = self.new_paged_plan(cached.numel(), max_new)
         kvk_paged_plan(self.handle, cached, new, free_pages, free_count, block_table, page_tokens,
                        max_new, out.seq_lens, out.q_start, out.slots, out.positions,
                        out.free_count, stream=stream)
@@ -693,10 +702,12 @@ class Layout:
         if not 0 <= layer < len(self.anchor):
             raise KvkError("kvk_mla_chunk", 1)
         d = self.d[self.anchor[layer]]
-        if out is None:
-            out = torch.empty(N, H, d, dtype=q_lat.dtype, device=q_lat.device)
-        if workspace is None:
-            workspace = self.new_chunk_workspace(layer, N, seq_lens.numel(), H)
+        if out is None or workspace is None:
+            with _on(stream):
+                if out is None:
+                    out = torch.empty(N, H, d, dtype=q_lat.dtype, device=q_lat.device)
+                if workspace is None:
+                    workspace = self.new_chunk_workspace(layer, N, seq_lens.numel(), H)
         _mla_chunk(self.handle, layer, d, self.d_rope, q_lat, q_rope, q_start, seq_lens,
                    block_table, page_tokens, softmax_scale, out, workspace, lse, stream)
         return out

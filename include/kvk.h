@@ -402,7 +402,8 @@ kvk_status kvk_absorb(const void* x, int x_dtype, int64_t x_stride_seq, int64_t 
  *   dev_positions    nullable out, int32 [max_new]: its position in its sequence (0 behind the
  *                    last token)
  *   dev_free_count_out  out, int32: count less the pages taken (0 at least); may be dev_free_count
- * dev_seq_lens and dev_q_start must not overlap the inputs.
+ * No result may overlap an input or another result (KVK_ERR_INVALID_ARG), dev_free_count_out on
+ * dev_free_count excepted.
  *
  * Negative lengths count as 0, tokens that do not fit the table row or max_new get no slot
  * (KVK_FLAG_SEQ_LEN).  A page that the free list cannot give, or an id outside the pool, leaves
@@ -452,7 +453,8 @@ kvk_status kvk_paged_write(kvk_layout* layout, int layer, const void* c_kv, int 
  *   q_lat        device, element (row, head, k) at q_lat[row * q_lat_stride_tok +
  *                head * q_lat_stride_head + k], k < d; q_rope likewise, k < d_rope.  dtype
  *                KVK_BF16, KVK_F16 or KVK_F32; strides in elements, multiples of 8
- *   n_q          rows of the query and output tensors; n_q * n_heads < 2^31 (0: nothing launched)
+ *   n_q          rows of the query and output tensors; n_q * n_heads <= 2^31 - 256 (0: nothing
+ *                launched)
  *   dev_q_start  device int32 [batch + 1], ascending within [0, n_q]; otherwise KVK_FLAG_SEQ_LEN
  *                and the call writes nothing
  *   dev_seq_lens device int32 [batch], clamped to [0, table_pages * page_tokens] (and 2^30;
@@ -465,8 +467,8 @@ kvk_status kvk_paged_write(kvk_layout* layout, int layer, const void* c_kv, int 
  *                run at the same time need one each.
  *
  * A token whose cached row is not finite (KVK_FLAG_NONFINITE at its write) turns the rows that
- * see it into NaN and no others.  Group-scaled values and f16 queries are held to the f16 range
- * by the tensor-core kernel.  That kernel takes bf16 queries (and f16 ones, except over
+ * see it into NaN and no others; scores of finite rows have to stay within fp32.  Group-scaled
+ * values and f16 queries are held to the f16 range by the tensor-core kernel.  That kernel takes bf16 queries (and f16 ones, except over
  * uncompressed anchors) with d <= 512, d_rope <= 64 and d_rope % 16 == 0; other calls take the
  * CUDA-core kernel.  kvk_set_decode_path and kvk_set_wait_limit apply.
  */
@@ -479,8 +481,11 @@ kvk_status kvk_mla_chunk(kvk_layout* layout, int layer, const void* q_lat, const
                          int64_t out_stride_head, float* lse, void* workspace,
                          size_t workspace_bytes, kvk_stream_t stream);
 
-/* Bytes of device workspace kvk_mla_chunk needs (it does not grow with n_q or batch today; pass
- * the call's). */
+/* Bytes of device workspace for a kvk_mla_chunk of these sizes: partial results, a fixed size, and
+ * from two tiles of 128 rows (query token, head) per sequence on (one over bf16 anchors) room for
+ * the pool's rows expanded to 16-bit operands, up to 2 (d + d_rope) bytes a slot and twice that
+ * for 16-bit or group-scaled codes.  A call that gets less than this, but no less than the size for
+ * n_q = 0, converts the rows inside the attention, tile by tile; below that KVK_ERR_WORKSPACE. */
 kvk_status kvk_chunk_workspace_bytes(const kvk_layout* layout, int layer, int n_q, int batch,
                                      int n_heads, size_t* bytes);
 

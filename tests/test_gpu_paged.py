@@ -112,12 +112,10 @@ def test_plan_updates_the_free_count_in_place(pkg):
         free, count = i32(list(range(40))), i32([40])
         cached = i32([0, 0])
         out = lay.new_paged_plan(2, 64)._replace(free_count=count)
-        seen = []
         for step in range(20):   # each step's lengths are the next step's cached ones
             p = lay.paged_plan(cached, i32([3, 17]), free, count, table, 16, 64, out=out)
             cached = p.seq_lens.clone()
-            seen.append(int(count))
-        assert cached.tolist() == [60, 340][:0] or cached.tolist() == [60, min(340, 320)]
+        assert cached.tolist() == [60, 320]          # the table row ends at 320
         used = table[table >= 0].tolist()
         assert len(used) == len(set(used))
         assert int(count) == 40 - len(used)
