@@ -38,9 +38,10 @@
 //
 // Numbers.  Codes enter the MMA exactly: a code of at most 8 bits is an f16 integer; a 16-bit
 // code c and a group-scaled value c s are split into two f16 parts (hi = f16(x), lo = x - hi)
-// whose score MMAs add up.  The output MMA takes the high part (relative 2^-12) and P in f16
-// (2^-12); bf16 rows stay bf16, P too (2^-9, as the rows' own rounding).  A bf16 query is scaled
-// by a power of two of its row into f16's range (exact but for elements 2^-38 below the largest).
+// whose score MMAs add up.  The output MMA takes the high part (at most 2^-11 of the value) and P
+// in f16 (2^-11); bf16 rows stay bf16, P too (2^-8, as the rows' own rounding).  A bf16 query is
+// scaled by a power of two of its row into f16's range: exact but for elements far below the
+// row's largest, which f16's subnormals leave off by at most 2^-39 of it.
 // Scores, references and sums are fp32.
 //
 // Softmax with token scales.  With z_t the score in log2 units and s_t the token's scale, the
@@ -782,7 +783,9 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
               // any positive scale serves
               const float w = v == 0.0f ? 5.9604644775390625e-8f : v;
               T.sc[x] = real ? v : 0.0f;
-              T.isc[x] = real ? __frcp_rn(w) : 0.0f;
+              // (a scale that is not finite shows in the weight of those who see the token; here
+              // it would reach, times a weight of 0, those who do not)
+              T.isc[x] = real && isfinite(w) ? __frcp_rn(w) : 0.0f;
               T.lsc[x] += log2f(w);
             }
           }
@@ -1285,6 +1288,18 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         m = mx;
       }
       const float mref = m == -CUDART_INF_F ? 0.0f : m;
+      // The previous output MMA has to have read P and left O before this block's P is written.
+      // Waited for ahead of the exponentials, but over bf16 rows (one score MMA a block, softmax
+      // the longer side) behind the first of them; us ahead / behind, expanded rows, d = 512: 8
+      // bits (1.35 TFLOP) 1140 / 1152, groups of 32 (0.15) 318 / 330, bf16 (2.9) 2570 / 2355.
+      auto pv_before = [&]() {
+        if (g == 0) return true;
+        if (!__all_sync(0xffffffffu, wait(&S.pv_done, (g - 1) & 1))) return false;
+        tc_fence_after();
+        return true;
+      };
+      if (!kBf16) ok = pv_before();
+      if (!ok) break;
 #pragma unroll 1
       for (int c0 = 0; c0 < kCols; c0 += 32) {
         if (kCols > 32) weights(c0, s);
@@ -1311,11 +1326,8 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
           pk[2 * i + 1] = pack_out(kBf16, e[2], e[3]);
         }
         l += l0 + l1;
-        if (c0 == 0 && g > 0) {                       // the previous output MMA has read P, left O
-          ok = __all_sync(0xffffffffu, wait(&S.pv_done, (g - 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-        }
+        if (kBf16 && c0 == 0) ok = pv_before();
+        if (!ok) break;
         const uint32_t row = p_s + (uint32_t)hh * kAtom + (uint32_t)r * 128u;
         const int c1 = (kCols * cg + c0) >> 3;        // first 16-byte chunk of the row
 #pragma unroll
