@@ -141,6 +141,16 @@ def _row_stride(t, dim=0):
     return (inner + 7) // 8 * 8
 
 
+def _strides3(t, name):
+    """Row and head stride of [rows, heads, width] with contiguous width, and its shape."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or (shape[2] > 1 and strides[2] != 1):
+        raise ValueError(f"{name} must be [rows, heads, width] with contiguous width")
+    if shape[0] > 1 and shape[1] > 1 and shape[2] > 0:
+        return strides[0], strides[1], shape
+    return _row_stride(t), _row_stride(t, 1), shape
+
+
 def _need_cuda(t, name, dtypes=None):
     if t is None:
         return
@@ -488,26 +498,24 @@ def _mla_chunk(handle, layer, d, d_rope, q_lat, q_rope, q_start, seq_lens, block
         raise _bad(seq_lens, "seq_lens", _I32, dev)
     if not (block_table.get_device() == dev and block_table.dtype is i32):
         raise _bad(block_table, "block_table", _I32, dev)
-    for t in (q_lat, q_rope, out):
-        if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-            raise ValueError("q_lat, q_rope and out must be [rows, heads, width] with contiguous "
-                             "width")
+    ql_t, ql_h, (N, H, width) = _strides3(q_lat, "q_lat")
+    qr_t, qr_h, qr_shape = _strides3(q_rope, "q_rope")
+    o_t, o_h, o_shape = _strides3(out, "out")
     if block_table.dim() != 2 or block_table.stride(1) != 1:
         raise ValueError("block_table must be [batch, pages] with contiguous rows")
-    N, H, width = q_lat.shape
     B = seq_lens.numel()
     rows, pages = block_table.shape
-    if q_rope.shape[:2] != (N, H) or out.shape[:2] != (N, H) or q_start.numel() < B + 1 or \
-            rows != B or (lse is not None and tuple(lse.shape) != (N, H)):
+    if qr_shape[0] != N or qr_shape[1] != H or o_shape[0] != N or o_shape[1] != H or \
+            q_start.numel() < B + 1 or rows != B or (lse is not None and lse.shape != (N, H)):
         raise ValueError("shapes of the queries, outputs, lengths and block table do not match")
-    if width < d or out.shape[2] < d or q_rope.shape[2] < d_rope:
+    if width < d or o_shape[2] < d or qr_shape[2] < d_rope:
         raise ValueError("q_lat, q_rope or out is narrower than the layer's rows")
     st = _lib_handle().kvk_mla_chunk(
-        handle, layer, q_lat.data_ptr(), q_rope.data_ptr(), _DTYPE[dtype], _row_stride(q_lat),
-        _row_stride(q_lat, 1), _row_stride(q_rope), _row_stride(q_rope, 1), N, B, H,
+        handle, layer, q_lat.data_ptr(), q_rope.data_ptr(), _DTYPE[dtype], ql_t, ql_h, qr_t, qr_h,
+        N, B, H,
         q_start.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), pages,
         block_table.stride(0) if B > 1 else pages, page_tokens, softmax_scale, out.data_ptr(),
-        _row_stride(out), _row_stride(out, 1), None if lse is None else lse.data_ptr(),
+        o_t, o_h, None if lse is None else lse.data_ptr(),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
     if st:
         raise KvkError("kvk_mla_chunk", st)
@@ -677,8 +685,11 @@ class Layout:
         place, free_pages[:free_count] is the free list, max_new bounds the new tokens of the
         batch.  Returns a PagedPlan (out, if one is given)."""
         if out is None:
-            with _on(stream):
-                out = self.new_paged_plan(cached.numel(), max_new)
+            if stream is not None:
+                with _on(stream):
+                    return self.paged_plan(cached, new, free_pages, free_count, block_table,
+                                           page_tokens, max_new)
+            out = self.new_paged_plan(cached.numel(), max_new)
         kvk_paged_plan(self.handle, cached, new, free_pages, free_count, block_table, page_tokens,
                        max_new, out.seq_lens, out.q_start, out.slots, out.positions,
                        out.free_count, stream=stream)
@@ -698,16 +709,19 @@ class Layout:
                   softmax_scale, out=None, lse=None, workspace=None, stream=None):
         """Causal attention of packed query rows over the paged cache (kvk_mla_chunk); returns
         out [N, H, d] of the queries' dtype."""
-        N, H = q_lat.shape[0], q_lat.shape[1]
+        N, H = q_lat.shape[:2]
         if not 0 <= layer < len(self.anchor):
             raise KvkError("kvk_mla_chunk", 1)
         d = self.d[self.anchor[layer]]
-        if out is None or workspace is None:
+        if stream is not None and (out is None or workspace is None):
             with _on(stream):
-                if out is None:
-                    out = torch.empty(N, H, d, dtype=q_lat.dtype, device=q_lat.device)
-                if workspace is None:
-                    workspace = self.new_chunk_workspace(layer, N, seq_lens.numel(), H)
+                return self.mla_chunk(
+                    layer, q_lat, q_rope, q_start, seq_lens, block_table, page_tokens,
+                    softmax_scale, out, lse, workspace)
+        if out is None:
+            out = q_lat.new_empty((N, H, d))
+        if workspace is None:
+            workspace = self.new_chunk_workspace(layer, N, seq_lens.numel(), H)
         _mla_chunk(self.handle, layer, d, self.d_rope, q_lat, q_rope, q_start, seq_lens,
                    block_table, page_tokens, softmax_scale, out, workspace, lse, stream)
         return out
