@@ -303,9 +303,11 @@ cudaError_t launch_tt_r(const ChunkArgs& a, int dtype, size_t smem, cudaStream_t
 #define KVK_LAUNCH(T)                                                                   \
   do {                                                                                  \
     auto k = chunk_fma_kernel<TT, R, T>;                                                \
-    static const cudaError_t room =                                                     \
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax); \
-    if (room != cudaSuccess) return room;                                               \
+    static std::atomic<uint64_t> done{0};                                               \
+    e = once_per_device(done, [&] {                                                     \
+      return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax); \
+    });                                                                                 \
+    if (e != cudaSuccess) return e;                                                     \
     e = cudaLaunchKernelEx(&cfg, k, a);                                                 \
     if (e != cudaSuccess) return e;                                                     \
   } while (0)

@@ -1546,13 +1546,15 @@ cudaError_t launch(const TcChunk& P, const CUtensorMap& hi, const CUtensorMap& l
                    cudaStream_t st) {
   auto k = chunk_tc_kernel<BITS, GROUP, kExp>;
   // the kernel hands registers from warpgroup to warpgroup: their number at launch is part of it
-  static const bool ready = [&] {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = once_per_device(done, [&] {
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, k) == cudaSuccess && at.numRegs == (int)kLaunchRegs &&
-           cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) ==
-               cudaSuccess;
-  }();
-  if (!ready) return cudaErrorInvalidValue;
+    const cudaError_t r = cudaFuncGetAttributes(&at, k);
+    if (r != cudaSuccess) return r;
+    if (at.numRegs != (int)kLaunchRegs) return cudaErrorNotSupported;
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+  });
+  if (e != cudaSuccess) return e;
   k<<<dim3(2 * P.w.G), dim3(kThreads), smem, st>>>(P, hi, lo);
   return cudaGetLastError();
 }

@@ -379,7 +379,7 @@ cudaError_t launch_write(const kvk_layout* L, const AnchorDesc& A, const T* c_kv
   const dim3 block(kWarpsPerBlock * 32);
   if (A.n <= kFastElems) {
     const int per = 4 * kWarpsPerBlock;
-    const dim3 grid((unsigned)((n_tokens + per - 1) / per));
+    const dim3 grid((unsigned)(((int64_t)n_tokens + per - 1) / per));
 #define KVK_FAST(B, G)                                                                       \
   paged_write_fast_kernel<T, B, G><<<grid, block, 0, st>>>(codes, scales, A.row_bytes, A.d,   \
                                                            L->d_rope, group, A.sg, pool, c_kv, \
@@ -396,7 +396,7 @@ cudaError_t launch_write(const kvk_layout* L, const AnchorDesc& A, const T* c_kv
     else KVK_FAST(16, false);
 #undef KVK_FAST
   } else {
-    const dim3 grid((unsigned)((n_tokens + kWarpsPerBlock - 1) / kWarpsPerBlock));
+    const dim3 grid((unsigned)(((int64_t)n_tokens + kWarpsPerBlock - 1) / kWarpsPerBlock));
     paged_write_kernel<T><<<grid, block, 0, st>>>(codes, scales, A.row_bytes, A.d, L->d_rope, A.b,
                                                   group, A.sg, pool, c_kv, c_st, k_rope, kr_st,
                                                   n_tokens, slots, flags);
@@ -416,10 +416,12 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = sizeof(int32_t) * (4 * (size_t)a.batch + 1);
-  static const cudaError_t room = cudaFuncSetAttribute(
-      paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      (int)sizeof(int32_t) * (4 * kMaxPagedBatch + 1));
-  if (room != cudaSuccess) return room;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = once_per_device(done, [] {
+    return cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(int32_t) * (4 * kMaxPagedBatch + 1));
+  });
+  if (e != cudaSuccess) return e;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -428,7 +430,7 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, paged_plan_kernel, a);
+  e = cudaLaunchKernelEx(&cfg, paged_plan_kernel, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

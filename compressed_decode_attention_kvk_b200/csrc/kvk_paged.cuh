@@ -7,9 +7,25 @@
 // power of two).  Position t of sequence i lives in slot table[i][t / P] * P + t % P.
 #pragma once
 
+#include <atomic>
+
 #include "kvk_internal.cuh"
 
 namespace kvk {
+
+// A kernel's attributes belong to a device: `set` runs once on each that launches it (and again
+// after a failure).  `done` is the kernel's own, a bit per device.
+template <typename F>
+cudaError_t once_per_device(std::atomic<uint64_t>& done, F set) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = set();
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 constexpr int kMaxPagedBatch = 4096;
 

@@ -550,3 +550,38 @@ def test_wait_limit_stops_the_kernel(pkg, oracle_mod):
             assert lay.read_status() == 0
     finally:
         lay.close()
+
+
+@pytest.mark.parametrize("path", [1, 2], ids=["tensor", "cuda_core"])
+def test_largest_batch_and_head_count(pkg, oracle_mod, path):
+    rng = np.random.default_rng(3)
+    lens = rng.integers(0, 3, 4096).tolist()
+    q_lens = [int(x) for x in rng.integers(0, 2, 4096)]
+    pool = Pool(pkg, oracle_mod, lens, 16, 0, 8, 0, 2, 2)
+    try:
+        ql, qr = pool.queries(q_lens, 1, torch.bfloat16, 1)
+        out, lse = _run(pool, pkg, path, q_lens, ql, qr, 0.2, torch.bfloat16)
+        pool.check(q_lens, ql, qr, out, lse, torch.bfloat16, 0.2, path == 1)
+    finally:
+        pool.lay.close()
+    pool = Pool(pkg, oracle_mod, [5, 70], 32, 16, 4, 0, 8, 2)
+    try:
+        ql, qr = pool.queries([1, 2], 4096, torch.bfloat16, 1)
+        out, lse = _run(pool, pkg, path, [1, 2], ql, qr, 0.2, torch.bfloat16)
+        pool.check([1, 2], ql, qr, out, lse, torch.bfloat16, 0.2, path == 1)
+    finally:
+        pool.lay.close()
+
+
+@pytest.mark.parametrize("page", [1, 4, 65536])
+@pytest.mark.parametrize("q_len", [2, 70])
+def test_smallest_and_largest_pages(pkg, oracle_mod, page, q_len):
+    pool = Pool(pkg, oracle_mod, [131, 300], 64, 32, 8, 0, page, 6)
+    try:
+        ql, qr = pool.queries([q_len, q_len], 10, torch.bfloat16, 1)
+        for path in (pkg.KVK_PATH_CUDA_CORE, pkg.KVK_PATH_TENSOR):
+            out, lse = _run(pool, pkg, path, [q_len, q_len], ql, qr, 0.1, torch.bfloat16)
+            pool.check([q_len, q_len], ql, qr, out, lse, torch.bfloat16, 0.1,
+                       path == pkg.KVK_PATH_TENSOR, f"path {path}")
+    finally:
+        pool.lay.close()
