@@ -1422,10 +1422,15 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
 constexpr int kMergeWarps = 8;
 constexpr int kMergeRounds = 4;   // pieces of a tile in rounds of 32 lanes: up to 127 clusters
 
-// CTA (g, y): if the last piece of cluster g began a tile it did not finish, rows 8 y .. 8 y + 7
-// (one a warp) of that tile, whose further pieces are the first ones of clusters g + 1, ... up to
-// the one that ends it.  A lane holds reference and sum of one piece a round; the outputs are then
-// added up piece by piece, 4 features a lane and 128, their loads independent of one another.
+// CTA (g, y, z): if the last piece of cluster g began a tile it did not finish, rows 8 y .. 8 y + 7
+// (one a warp) of that tile and kF x 128 of its features, whose further pieces are the first ones
+// of clusters g + 1, ... up to the one that ends it.  A lane holds reference and sum of one piece a
+// round; the outputs are then added up piece by piece, their loads independent of one another.
+// kF = 4 takes all features in one warp; kF = 1 spreads them over d / 128 CTAs, for tiles of many
+// pieces, at the price of the CTAs that find no work (decode calls, kF = 4 / 1, us: one sequence of
+// 8192 tokens 66.0 / 56.8, of 32768 93.5 / 82.5, of 64 25.0 / 26.5; 4 of 8192 50.5 / 50.4; 8 of 4096
+// 46.8 / 47.3).
+template <int kF>
 __global__ void __launch_bounds__(kMergeWarps * 32)
 chunk_merge_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ ChunkWork w,
                    int q_bf16) {
@@ -1480,27 +1485,27 @@ chunk_merge_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ 
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-  float4 acc[4];                          // d <= 512
+  const int f0 = 128 * kF * blockIdx.z + 4 * lane;
+  float4 acc[kF];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < kF; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int r = 0; r < kMergeRounds; ++r) {
     const int top = min(32, n - 32 * r);
-#pragma unroll 4
+#pragma unroll (kF == 1 ? 8 : 4)
     for (int i = 0; i < top; ++i) {
       const float x = __shfl_sync(0xffffffffu, m[r], i);
-      if (x == 0.0f) continue;            // no piece, or no weight
+      if (kF > 1 && x == 0.0f) continue;
       const float* o = w.o + slot(32 * r + i) * a.d;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int f = 128 * k + 4 * lane;
-        if (f < a.d) {
-          const float4 v = *reinterpret_cast<const float4*>(o + f);
-          acc[k].x = fmaf(x, v.x, acc[k].x);
-          acc[k].y = fmaf(x, v.y, acc[k].y);
-          acc[k].z = fmaf(x, v.z, acc[k].z);
-          acc[k].w = fmaf(x, v.w, acc[k].w);
-        }
+      for (int k = 0; k < kF; ++k) {
+        const int f = 128 * k + f0;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);   // x = 0: no piece, or no weight
+        if (x != 0.0f && f < a.d) v = *reinterpret_cast<const float4*>(o + f);
+        acc[k].x = fmaf(x, v.x, acc[k].x);
+        acc[k].y = fmaf(x, v.y, acc[k].y);
+        acc[k].z = fmaf(x, v.z, acc[k].z);
+        acc[k].w = fmaf(x, v.w, acc[k].w);
       }
     }
   }
@@ -1508,14 +1513,14 @@ chunk_merge_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ 
   uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(h.row0 + j) * a.o_st +
                   (int64_t)hd * a.o_sh;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int f = 128 * k + 4 * lane;
+  for (int k = 0; k < kF; ++k) {
+    const int f = 128 * k + f0;
     if (f < a.d)
       *reinterpret_cast<uint2*>(out + f) =
           make_uint2(pack_out(q_bf16, acc[k].x * inv, acc[k].y * inv),
                      pack_out(q_bf16, acc[k].z * inv, acc[k].w * inv));
   }
-  if (a.lse && lane == 0)
+  if (a.lse && lane == 0 && blockIdx.z == 0)
     a.lse[(int64_t)(h.row0 + j) * a.H + hd] = L == 0.0f ? -CUDART_INF_F : kLn2 * (M + log2f(L));
 }
 
@@ -1635,8 +1640,13 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkWork& w, int dtype, c
   }
   if (e != cudaSuccess) return e;
   // a programmatic dependent: its CTAs are in place when the partials are
-  e = launch_pdl(chunk_merge_kernel, dim3(w.G, 128 / kMergeWarps), dim3(kMergeWarps * 32), 0, st, a, w,
-                 P.q_bf16);
+  // features spread where a tile may have sixteen pieces or more, were each sequence one tile
+  if (a.batch <= w.G / 16 && a.cap >= 16 * 128)
+    e = launch_pdl(chunk_merge_kernel<1>, dim3(w.G, 128 / kMergeWarps, (a.d + 127) / 128),
+                   dim3(kMergeWarps * 32), 0, st, a, w, P.q_bf16);
+  else
+    e = launch_pdl(chunk_merge_kernel<4>, dim3(w.G, 128 / kMergeWarps), dim3(kMergeWarps * 32), 0, st, a,
+                   w, P.q_bf16);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
