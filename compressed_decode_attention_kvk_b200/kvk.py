@@ -442,8 +442,21 @@ def kvk_paged_plan(handle, cached, new, free_pages, free_count, block_table, pag
 
 
 def kvk_paged_write(handle, layer, c_kv, k_rope, slots, stream=None):
-    """c_kv [N, >=d], k_rope [N, d_rope] (fp32 or bf16, CUDA, last dim contiguous) quantised to
+    """c_kv [N, >=d], k_rope [N, >=d_rope] (fp32 or bf16, CUDA, last dim contiguous) quantised to
     slots int32 [>= N] of the layer's pool (negative: skipped)."""
+    info = _layer_info(handle, layer)
+    _paged_write(handle, layer, info.d, info.d_rope, c_kv, k_rope, slots, stream)
+
+
+def _paged_write(handle, layer, d, d_rope, c_kv, k_rope, slots, stream):
+    """kvk_paged_write for a caller that knows the layer's widths (the library sees strides only:
+    narrower rows would be read past their ends)."""
+    if c_kv.dim() != 2 or k_rope.dim() != 2:
+        raise ValueError("c_kv / k_rope must be [tokens, width] with contiguous width")
+    N, width = c_kv.shape
+    rope_rows, rope_width = k_rope.shape
+    if width < d or rope_width < d_rope:
+        raise ValueError(f"c_kv or k_rope is narrower than the layer's rows ({d} and {d_rope})")
     dtype, dev = c_kv.dtype, _current_device(c_kv, "c_kv")
     if not (c_kv.get_device() == dev and dtype in _KV_TYPES):
         raise _bad(c_kv, "c_kv", _KV_TYPES, dev)
@@ -451,11 +464,9 @@ def kvk_paged_write(handle, layer, c_kv, k_rope, slots, stream=None):
         raise _bad(k_rope, "k_rope", (dtype,), dev)
     if not (slots.get_device() == dev and slots.dtype is torch.int32 and slots.is_contiguous()):
         raise _bad(slots, "slots", _I32, dev)
-    if c_kv.dim() != 2 or k_rope.dim() != 2 or (c_kv.shape[1] > 1 and c_kv.stride(1) != 1) or \
-            (k_rope.shape[1] > 1 and k_rope.stride(1) != 1):
+    if (width > 1 and c_kv.stride(1) != 1) or (rope_width > 1 and k_rope.stride(1) != 1):
         raise ValueError("c_kv / k_rope must be [tokens, width] with contiguous width")
-    N = c_kv.shape[0]
-    if k_rope.shape[0] != N or slots.numel() < N:
+    if rope_rows != N or slots.numel() < N:
         raise ValueError("k_rope and slots must cover c_kv's tokens")
     st = _lib_handle().kvk_paged_write(handle, layer, c_kv.data_ptr(), _DTYPE[dtype],
                                        _row_stride(c_kv), k_rope.data_ptr(), _row_stride(k_rope),
@@ -696,7 +707,10 @@ class Layout:
         return out
 
     def paged_write(self, layer, c_kv, k_rope, slots, stream=None):
-        kvk_paged_write(self.handle, layer, c_kv, k_rope, slots, stream=stream)
+        if not 0 <= layer < len(self.anchor):
+            raise KvkError("kvk_paged_write", 1)
+        _paged_write(self.handle, layer, self.d[self.anchor[layer]], self.d_rope, c_kv, k_rope,
+                     slots, stream)
 
     def chunk_workspace_bytes(self, layer, n_q, batch, n_heads):
         return kvk_chunk_workspace_bytes(self.handle, layer, n_q, batch, n_heads)

@@ -76,3 +76,28 @@ def test_row_stride_of_single_rows(kvk):
     assert kvk._row_stride(one) % 8 == 0 and kvk._row_stride(one) >= 64
     assert kvk._row_stride(x[:, :, :0]) == 0
     assert kvk._row_stride(x.expand(3, 5, 64)[:, :1]) == 320
+
+
+@pytest.mark.parametrize("through", ["function", "layout"])
+@pytest.mark.parametrize("width,rope", [(63, 16), (32, 16), (0, 16), (64, 15), (64, 0), (8, 8)])
+def test_write_refuses_rows_narrower_than_the_layer(kvk, lay, through, width, rope):
+    """A row of fewer than d (or d_rope) elements would be read into the next one, the last past
+    the tensor's end; the library sees strides only, so the binding has to refuse it."""
+    c, kr = torch.zeros(4, width), torch.zeros(4, rope)
+    slots = torch.zeros(4, dtype=torch.int32)
+    if through == "function":
+        def write(*a):
+            kvk.kvk_paged_write(lay, 0, *a)
+    else:
+        L = object.__new__(kvk.Layout)   # the layout's widths without its arena
+        L.anchor, L.d, L.d_rope, L.handle = [0, 0], [64, 0], 16, None
+
+        def write(*a):
+            L.paged_write(0, *a)
+    with pytest.raises(ValueError, match="narrower"):
+        write(c, kr, slots)
+    # rows that are wide enough get as far as the check of their device
+    with pytest.raises(ValueError, match="CUDA"):
+        write(torch.zeros(4, 64), torch.zeros(4, 16), slots)
+    with pytest.raises(ValueError, match="CUDA"):
+        write(torch.zeros(4, 80), torch.zeros(4, 24), slots)
