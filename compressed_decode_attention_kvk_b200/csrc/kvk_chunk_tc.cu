@@ -62,6 +62,7 @@
 #include <algorithm>
 
 #include "kvk_chunk_convert.cuh"
+#include "kvk_chunk_stop.cuh"
 #include "kvk_chunk_tc.cuh"
 #include "kvk_decode_common.cuh"
 #include "kvk_sm100.cuh"
@@ -84,6 +85,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;          // growth of a row's maximum that its reference lets pass
 constexpr int kSmemLimit = 232448;
 constexpr int kMaxK = 8;               // slots of the K ring, two atoms each
+constexpr int kStep = 2;               // atoms of a K ring slot
 constexpr uint64_t kDrainLimitNs = 2000000000ull;
 
 constexpr uint32_t kLaunchRegs = 65536 / kThreads;
@@ -119,6 +121,7 @@ struct Shared {
   int64_t scan[kWarps + 1];
   int64_t start_base;
   int32_t start_seq, start_k;
+  int32_t issued[2];                   // steps whose loads this CTA has issued: K, V
   uint32_t tmem_base, abort_word;
 };
 
@@ -156,11 +159,17 @@ struct TcChunk {
   int pool_slots;
 };
 
-// A stopped kernel's copies: waits for a phase that its loads complete.
-__device__ __forceinline__ void drain(uint64_t* b, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_hint(b, parity, 20000u) && globaltimer() - t0 < kDrainLimitNs) {
+// At a kernel's end: waits, until the clock shows `end` at the latest, for a phase that operations
+// in flight complete.
+__device__ __forceinline__ void drain(uint64_t* b, uint32_t parity, uint64_t end) {
+  while (!mbar_try_hint(b, parity, 20000u) && globaltimer() < end) {
   }
+}
+// Counts bytes as landed that no load brings (a stopped kernel's).
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* b, uint32_t tx) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)),
+               "r"(tx)
+               : "memory");
 }
 
 // ---- cluster-scope barriers -----------------------------------------------------------------
@@ -263,6 +272,34 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* tmap, in
       "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+
+// A stopped kernel's loads (kvk_chunk_stop.cuh): the leader waits for those of both CTAs, which have
+// left their loops.  One deadline for all of them.
+template <bool kLo>
+__device__ __forceinline__ void finish_loads(const TcChunk& P, Shared& S, int nch) {
+  const uint64_t end = globaltimer() + kDrainLimitNs;
+  const int atoms = P.NA * (kLo ? 2 : 1), steps = (atoms + kStep - 1) / kStep;   // of a block
+#pragma unroll 1
+  for (int ring = 0; ring < 2; ++ring) {
+    const int slots = ring == 0 ? P.NK : P.NVS * nch, own = S.issued[ring];
+    int peer;
+    asm volatile("ld.volatile.shared::cluster.s32 %0, [%1];"
+                 : "=r"(peer)
+                 : "r"(map_rank(smem_u32(&S.issued[ring]), 1))
+                 : "memory");
+#pragma unroll 1
+    for (int i = stop_first(slots, own, peer); i < max(own, peer); ++i) {
+      const StopStep t = stop_step(i, slots, own, peer);
+      const int ch = t.slot % nch;
+      uint64_t* bar = ring == 0 ? &S.k_ready[t.slot] : &S.v_ready[t.slot / nch * 2 + ch];
+      // a CTA's atoms of the step (V: for both halves of the block's tokens)
+      const int n = ring == 0 ? min(kStep, atoms - kStep * (i % steps)) : 2 * min(2, P.NV - 2 * ch);
+      if (t.arm) mbar_arrive_expect_tx(bar, (uint32_t)n * kAtom);
+      if (t.complete) mbar_complete_tx(bar, (uint32_t)n * kAtom);
+      drain(bar, t.parity, end);
+    }
+  }
 }
 
 // Bounded waits of one call: a wait that runs out stops both CTAs.
@@ -473,7 +510,6 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
   // cost of a row tile beside its blocks, in blocks (a ragged batch of 16 over expanded rows: 951 us
   // with 2, 831 with 4, 822 with 6; decode of 32 sequences from packed rows: 230, 245, 250)
   constexpr int kCost = kExp ? 5 : 2;
-  constexpr int kStep = 2;                            // atoms of a K ring slot
   // the output MMAs' warp is the one that has no other work: the relay's with expanded rows, else
   // the loads'
   constexpr int kOutWarp = kExp ? kRelayWarp : kLoadWarp;
@@ -494,6 +530,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
 
   if (tid == 0) {
     S.abort_word = 0;
+    S.issued[0] = S.issued[1] = 0;
     for (int i = 0; i < kMaxTok; ++i) {
       mbar_init(&S.tok_full[i], 1);
       // softmax warps, loading or converting warps and relay, the leader's MMA warps
@@ -710,10 +747,10 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
           commit_both(&S.pv_done);
         }
       }
-      // every MMA and its arrivals are done before either CTA leaves
+      // every MMA is done before either CTA leaves
       __syncwarp();
       commit_both(&S.drain[scores ? 0 : 1]);
-      drain(&S.drain[scores ? 0 : 1], 0u);
+      drain(&S.drain[scores ? 0 : 1], 0u, globaltimer() + kDrainLimitNs);
     }
   } else if (warp == kTokWarp) {
     regs_set<kRegs3>();
@@ -926,7 +963,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
   } else if (warp == kLoadWarp) {
     regs_set<kRegs3>();
     // ======================= K loads (expanded rows) ============================================
-    int kslot = 0;
+    int kslot = 0, issued = 0;
     uint32_t kpar = 1;
     bool ok = kExp;
     while (ok) {
@@ -956,20 +993,19 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
           tma_load_pair(to + (uint32_t)(kslot * kStep) * kAtom, map, (kLo ? i >> 1 : i + j) * 64, sl,
                         map_rank(smem_u32(&S.k_ready[kslot]), 0));
         __syncwarp();
+        ++issued;
         if (++kslot == P.NK) {
           kslot = 0;
           kpar ^= 1;
         }
       }
     }
-    // loads in flight (only a stopped kernel has any) land before either CTA's memory goes
-    if (kExp && rank == 0 && lane == 0)
-      for (int j = 0; j < P.NK; ++j) drain(&S.k_ready[j], j < kslot ? kpar ^ 1 : kpar);
+    if (lane == 0) S.issued[0] = issued;
   } else if (kExp && warp >= kVWarp0) {
     regs_set<kRegs2>();
     // ======================= V loads (expanded rows), query rows ================================
     const int vw = warp - kVWarp0;
-    uint32_t armed = 0, landing = 0;                  // barriers used so far, and their last phase
+    int issued = 0;
     bool ok = true;
     for (int g = 0;; ++g) {
       const int st = ring.st;
@@ -1005,8 +1041,6 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
           ok = __all_sync(0xffffffffu, wait(&S.v_empty[vs * 2 + ch], vpar ^ 1));
           if (!ok) break;
           if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar, 2u * 2u * nj * kAtom);
-          armed |= 1u << (vs * 2 + ch);
-          landing = (landing & ~(1u << (vs * 2 + ch))) | vpar << (vs * 2 + ch);
 #pragma unroll 1
           for (int i = lane; i < per * nj; i += 32) {
             const int jj = i >= per, t = (i - jj * per) * P.box;
@@ -1017,15 +1051,14 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
                           sl < 0 ? P.pool_slots : sl, map_rank(smem_u32(bar), 0));
           }
           __syncwarp();
+          ++issued;
         }
         if (!ok) break;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.tok_empty[st]);
     }
-    if (vw == 0 && rank == 0 && lane == 0)
-      for (int j = 0; j < 4; ++j)
-        if (armed >> j & 1) drain(&S.v_ready[j], landing >> j & 1);
+    if (vw == 0 && lane == 0) S.issued[1] = issued;
   } else if (!kExp && warp >= kVWarp0) {
     regs_set<kRegs2>();
     // ======================= V team =============================================================
@@ -1404,12 +1437,26 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       tc_fence_before();
     }
   }
-  // a wait that ran out anywhere stops both CTAs; each reports it
+  // Every role of both CTAs is through.  A wait that ran out anywhere has stopped both: then loads
+  // may be in flight, into either CTA's memory, and both stay until the leader has seen them land.
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && abort_read(smem_u32(&S.abort_word))) atomicOr(a.flags, KVK_FLAG_TIMEOUT);
   cluster_sync();
+  if (abort_read(smem_u32(&S.abort_word))) {           // (the same in both CTAs)
+    if (tid == 0) atomicOr(a.flags, KVK_FLAG_TIMEOUT);
+    if constexpr (kExp) {
+      if (rank == 0 && tid == 0) finish_loads<kLo>(P, S, nch);
+      __syncthreads();
+      cluster_sync();
+    }
+  }
+  // the leader's last commits arrive here too: nothing is on its way to this memory any more
+  if (rank == 1 && tid == 0) {
+    const uint64_t end = globaltimer() + kDrainLimitNs;
+    drain(&S.drain[0], 0u, end);
+    drain(&S.drain[1], 0u, end);
+  }
   if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(kTmemCols)
