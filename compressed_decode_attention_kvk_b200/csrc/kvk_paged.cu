@@ -5,7 +5,10 @@
 // have_i = ceil(a_i / P) pages and needs need_i = ceil((a_i + f_i) / P); the pages it lacks come
 // off the end of the free list in sequence order, so the k-th page taken (k counted over the
 // whole batch) is free[count - 1 - k].  q_start is the exclusive prefix sum of the f_i, and the
-// new token at position t of sequence i goes to slot table[i][t / P] P + t % P.
+// new token at position t of sequence i goes to slot table[i][t / P] P + t % P.  Where the batch has
+// more new tokens than max_new, those behind it are none of the step's: no row, slot or page, and the
+// lengths end with the ones before, so that the attention over the offsets and lengths sees every row
+// at its token's position.
 //
 // One launch: every CTA computes both prefix sums itself (at most 4096 sequences, four a thread),
 // then the CTAs share out the pages taken and the tokens.  A new token's page is computed from the
@@ -22,14 +25,14 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCtas = 64, kPlanCluster = 8;   // most CTAs; most with the count updated in place
-constexpr int kPlanPer = kMaxPagedBatch / kPlanThreads;
 
 struct PlanSeq {
-  int cached, fresh, kept;   // clamped counts; kept: new tokens that fit the table row
+  int cached, fresh, kept;   // clamped counts; kept: new tokens that fit the table row and max_new
   int have, need;
   bool bad;
 };
-__device__ __forceinline__ PlanSeq plan_seq(const PlanArgs& a, int i) {
+// Sequence i with room for at most `room` new tokens.
+__device__ __forceinline__ PlanSeq plan_seq(const PlanArgs& a, int i, int64_t room) {
   const int c = __ldg(a.cached + i), f = __ldg(a.fresh + i);
   const int cap = (int)min((int64_t)a.table_pages << a.page_shift, (int64_t)0x7FFFFFFF);
   PlanSeq s;
@@ -37,6 +40,7 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanArgs& a, int i) {
   s.fresh = max(f, 0);
   s.kept = min(s.fresh, cap - s.cached);
   s.bad = s.cached != c || s.kept != f;
+  s.kept = (int)min((int64_t)s.kept, max(room, (int64_t)0));
   const int64_t r = (1 << a.page_shift) - 1;
   s.have = (int)((s.cached + r) >> a.page_shift);
   s.need = (int)((s.cached + (int64_t)s.kept + r) >> a.page_shift);
@@ -54,28 +58,9 @@ __device__ __forceinline__ int plan_page(const PlanArgs& a, int count, int64_t k
   return -1;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PlanArgs a) {
-  extern __shared__ int32_t plan_smem[];
-  int32_t* start_s = plan_smem;                     // [batch + 1] first new token of each sequence
-  int32_t* taken_s = start_s + a.batch + 1;         // [batch] pages taken before each sequence
-  int32_t* cached_s = taken_s + a.batch;            // [batch] its cached and its kept new tokens
-  int32_t* kept_s = cached_s + a.batch;
-  __shared__ int64_t warp_new[32], warp_page[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int count = min(max(__ldg(a.free_count), 0), a.free_capacity);
-
-  // prefix sums over the sequences, kPlanPer consecutive ones a thread
-  const int per = (a.batch + kPlanThreads - 1) / kPlanThreads;
-  const int i0 = min(a.batch, tid * per), i1 = min(a.batch, i0 + per);
-  int64_t fresh = 0, pages = 0;
-  bool bad = false;
-  for (int i = i0; i < i1; ++i) {
-    const PlanSeq s = plan_seq(a, i);
-    fresh += s.fresh;
-    pages += s.need - s.have;
-    bad = bad || s.bad;
-  }
-  int64_t x = fresh, y = pages;   // inclusive warp scans
+// Inclusive prefix sums of x and y over the block; x_all[31] and y_all[31] become the totals.
+__device__ __forceinline__ void plan_scan(int64_t& x, int64_t& y, int64_t* x_all, int64_t* y_all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
@@ -85,12 +70,12 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     }
   }
   if (lane == 31) {
-    warp_new[warp] = x;
-    warp_page[warp] = y;
+    x_all[warp] = x;
+    y_all[warp] = y;
   }
   __syncthreads();
   if (warp == 0) {
-    int64_t u = warp_new[lane], v = warp_page[lane];
+    int64_t u = x_all[lane], v = y_all[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t p = __shfl_up_sync(0xffffffffu, u, o), q = __shfl_up_sync(0xffffffffu, v, o);
@@ -99,16 +84,59 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
         v += q;
       }
     }
-    warp_new[lane] = u;
-    warp_page[lane] = v;
+    x_all[lane] = u;
+    y_all[lane] = v;
   }
   __syncthreads();
-  int64_t at = x - fresh + (warp ? warp_new[warp - 1] : 0);
-  int64_t page_at = y - pages + (warp ? warp_page[warp - 1] : 0);
-  const int64_t total = min(warp_new[31], (int64_t)a.max_new);
-  const int64_t taken = warp_page[31];
+  if (warp) {
+    x += x_all[warp - 1];
+    y += y_all[warp - 1];
+  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PlanArgs a) {
+  extern __shared__ int32_t plan_smem[];
+  int32_t* start_s = plan_smem;                     // [batch + 1] first new token of each sequence
+  int32_t* taken_s = start_s + a.batch + 1;         // [batch] pages taken before each sequence
+  int32_t* cached_s = taken_s + a.batch;            // [batch] its cached and its kept new tokens
+  int32_t* kept_s = cached_s + a.batch;
+  __shared__ int64_t warp_new[32], warp_page[32];
+  const int tid = threadIdx.x;
+  const int count = min(max(__ldg(a.free_count), 0), a.free_capacity);
+
+  // prefix sums over the sequences, a run of consecutive ones a thread: of the new tokens, and of the
+  // pages taken, first as though max_new held all the tokens
+  const int per = (a.batch + kPlanThreads - 1) / kPlanThreads;
+  const int i0 = min(a.batch, tid * per), i1 = min(a.batch, i0 + per);
+  const int64_t all = (int64_t)1 << 62;
+  int64_t fresh = 0, pages = 0;
+  bool bad = false;
   for (int i = i0; i < i1; ++i) {
-    const PlanSeq s = plan_seq(a, i);
+    const PlanSeq s = plan_seq(a, i, all);
+    fresh += s.fresh;
+    pages += s.need - s.have;
+    bad = bad || s.bad;
+  }
+  int64_t x = fresh, y = pages;
+  plan_scan(x, y, warp_new, warp_page);
+  const int64_t at0 = x - fresh;                    // new tokens before this thread's sequences
+  const int64_t asked = warp_new[31], total = min(asked, (int64_t)a.max_new);
+  if (asked > a.max_new) {                          // (the same in every thread)
+    pages = 0;
+    int64_t at = at0;
+    for (int i = i0; i < i1; ++i) {
+      const PlanSeq s = plan_seq(a, i, a.max_new - at);
+      at += s.fresh;
+      pages += s.need - s.have;
+    }
+    __syncthreads();                                // the sums have been read
+    x = fresh, y = pages;
+    plan_scan(x, y, warp_new, warp_page);
+  }
+  const int64_t taken = warp_page[31];
+  int64_t at = at0, page_at = y - pages;
+  for (int i = i0; i < i1; ++i) {
+    const PlanSeq s = plan_seq(a, i, a.max_new - at);
     start_s[i] = (int32_t)min(at, (int64_t)a.max_new);
     taken_s[i] = (int32_t)min(page_at, (int64_t)0x7FFFFFFF);
     cached_s[i] = s.cached;
@@ -120,13 +148,10 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
   __syncthreads();
 
   if (blockIdx.x == 0) {
-    if (bad || (tid == 0 && warp_new[31] > a.max_new)) atomicOr(a.flags, KVK_FLAG_SEQ_LEN);
+    if (bad || (tid == 0 && asked > a.max_new)) atomicOr(a.flags, KVK_FLAG_SEQ_LEN);
     for (int i = tid; i <= a.batch; i += kPlanThreads) {
       a.q_start[i] = start_s[i];
-      if (i < a.batch) {
-        const PlanSeq s = plan_seq(a, i);
-        a.seq_lens[i] = s.cached + s.kept;
-      }
+      if (i < a.batch) a.seq_lens[i] = cached_s[i] + kept_s[i];
     }
   }
   // the pages taken, one a thread

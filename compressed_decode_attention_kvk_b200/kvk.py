@@ -694,7 +694,8 @@ class Layout:
                    out=None, stream=None):
         """The pages and slots of a step's new tokens (kvk_paged_plan): block_table is updated in
         place, free_pages[:free_count] is the free list, max_new bounds the new tokens of the
-        batch.  Returns a PagedPlan (out, if one is given)."""
+        batch (those behind it are left out of every result, and flagged).  Returns a PagedPlan
+        (out, if one is given)."""
         if out is None:
             if stream is not None:
                 with _on(stream):

@@ -396,7 +396,7 @@ kvk_status kvk_absorb(const void* x, int x_dtype, int64_t x_stride_seq, int64_t 
  *   dev_block_table  the taken pages are written to the row's entries behind the held ones; no
  *                    other entry changes
  *   dev_seq_lens     out, int32 [batch]: a_i + f_i
- *   dev_q_start      out, int32 [batch + 1]: exclusive prefix sums of the f_i
+ *   dev_q_start      out, int32 [batch + 1]: exclusive prefix sums of the f_i, at most max_new
  *   dev_slots        out, int32 [max_new]: the slot of each new token, the sequences' tokens end
  *                    to end; entries behind the last token are -1
  *   dev_positions    nullable out, int32 [max_new]: its position in its sequence (0 behind the
@@ -405,9 +405,16 @@ kvk_status kvk_absorb(const void* x, int x_dtype, int64_t x_stride_seq, int64_t 
  * No result may overlap an input or another result (KVK_ERR_INVALID_ARG), dev_free_count_out on
  * dev_free_count excepted.
  *
- * Negative lengths count as 0, tokens that do not fit the table row or max_new get no slot
- * (KVK_FLAG_SEQ_LEN).  A page that the free list cannot give, or an id outside the pool, leaves
- * the entry at -1 and its tokens without slot (-1; KVK_FLAG_PAGE).
+ * Negative lengths count as 0 (KVK_FLAG_SEQ_LEN).  New tokens behind the first max_new of the batch
+ * are none of the step's (KVK_FLAG_SEQ_LEN): they get no row, slot or page, and dev_seq_lens ends
+ * with the tokens before them, so that attention over these results is that of the tokens kept.
+ * Tokens that do not fit the table row get no slot (KVK_FLAG_SEQ_LEN): dev_seq_lens is then
+ * table_pages * page_tokens, while dev_q_start counts all f_i rows, for the caller's packed rows are
+ * laid out so; kvk_mla_chunk takes a sequence's rows for the last ones before its length, so that
+ * this sequence's rows come out for earlier positions than their tokens' (seeing fewer tokens, all
+ * of them written), the other sequences' as ever.
+ * A page that the free list cannot give, or an id outside the pool, leaves the entry at -1 and its
+ * tokens without slot (-1; KVK_FLAG_PAGE); they count in dev_seq_lens, and kvk_mla_chunk skips them.
  */
 kvk_status kvk_paged_plan(kvk_layout* layout, const int32_t* dev_cached, const int32_t* dev_new,
                           int batch, const int32_t* dev_free_pages, const int32_t* dev_free_count,

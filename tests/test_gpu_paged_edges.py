@@ -7,8 +7,8 @@ import numpy as np
 import pytest
 import torch
 
-from paged_helpers import BF16_ROWS
-from test_gpu_paged import Pool, _run
+from paged_helpers import BF16_ROWS, check_chunk, chunk_reference, dequantised, random_table
+from test_gpu_paged import Pool, _run, _values, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -52,5 +52,119 @@ def test_a_stop_at_any_moment_ends_soon(pkg, oracle_mod, b, G, d):
         out, lse = _run(pool, pkg, pkg.KVK_PATH_TENSOR, q_lens, ql, qr, sigma, torch.bfloat16)
         pool.check(q_lens, ql, qr, out, lse, torch.bfloat16, sigma, True)
         assert lay.read_status() == 0
+    finally:
+        lay.close()
+
+
+# ---------------------------------------------------------------------------------------
+# steps that do not fit
+# ---------------------------------------------------------------------------------------
+
+def kept_plan(cached, new, free, count, table, page, max_new, pool_pages):
+    """The plan of the tokens that are kept: the first max_new of the batch, and of those what fits
+    the table row.  Returns (table, seq_lens, q_start, slots, positions, free count)."""
+    table = [list(r) for r in table]
+    cap = len(table[0]) * page
+    cnt = min(max(count, 0), len(free))
+    taken, row = 0, 0
+    seq_lens, q_start, slots, positions = [], [0], [-1] * max_new, [0] * max_new
+    for i, (a, f) in enumerate(zip(cached, new)):
+        a, rows = min(max(a, 0), cap), min(max(f, 0), max_new - row)
+        kept = min(rows, cap - a)
+        for k in range(-(-a // page), -(-(a + kept) // page)):
+            p = free[cnt - 1 - taken] if taken < cnt else -1
+            table[i][k] = p if 0 <= p < pool_pages else -1
+            taken += 1
+        for k in range(kept):
+            p = table[i][(a + k) // page]
+            positions[row + k] = a + k
+            slots[row + k] = p * page + (a + k) % page if 0 <= p < pool_pages else -1
+        row += rows
+        seq_lens.append(a + kept)
+        q_start.append(row)
+    return table, seq_lens, q_start, slots, positions, max(0, cnt - taken)
+
+
+@pytest.mark.parametrize("batch,max_new", [(1, 0), (3, 5), (40, 100), (300, 1), (1000, 2500), (4096, 9000)])
+def test_plan_keeps_the_first_max_new_tokens(pkg, batch, max_new):
+    rng = np.random.default_rng(batch + max_new)
+    page, width = 16, 6                              # rows of at most 96 tokens, some overflow
+    cached = rng.integers(0, 90, batch).tolist()
+    new = (rng.integers(0, 12, batch) * (rng.random(batch) < 0.8) + 1).astype(int).tolist()
+    n_pages = batch * width + 3
+    table = random_table(rng, cached, page, n_pages, width)
+    held = set(table.ravel().tolist())
+    free = [int(p) for p in rng.permutation(n_pages) if p not in held]
+    lay = pkg.Layout([0], [64], [4], 64, 16, 1, n_pages * page)
+    try:
+        t = i32(table.tolist())
+        p = lay.paged_plan(i32(cached), i32(new), i32(free), i32([len(free)]), t, page, max_new)
+        ref = kept_plan(cached, new, free, len(free), table.tolist(), page, max_new, n_pages)
+        got = (t.tolist(), p.seq_lens.tolist(), p.q_start.tolist(), p.slots.tolist(),
+               p.positions.tolist(), p.free_count.item())
+        for name, x, y in zip(("table", "seq_lens", "q_start", "slots", "positions", "free"), got, ref):
+            assert x == y, name
+        over = sum(new) > max_new or any(a + f > width * page for a, f in zip(cached, new))
+        assert lay.read_status(clear=True) == (pkg.KVK_FLAG_SEQ_LEN if over else 0)
+    finally:
+        lay.close()
+
+
+@pytest.mark.parametrize("path", [1, 2], ids=["tensor", "cuda_core"])
+@pytest.mark.parametrize("kind", ["max_new", "table_row"])
+def test_an_overflowing_step_through_plan_write_and_attention(pkg, oracle_mod, kind, path):
+    """More new tokens than max_new: the rows kept are those of their tokens' positions, nothing that
+    was not written is read.  More than a table row holds: that sequence's rows are the last ones
+    before the row's end, the other sequences are as ever."""
+    d, dR, H, page, b = 128, 64, 6, 16, 8
+    if kind == "max_new":
+        cached, new, max_new, width = [20, 5, 40], [3, 6, 2], 7, 4
+        lens, q_lens = [23, 9, 40], [3, 4, 0]
+    else:
+        cached, new, max_new, width = [20, 29, 7], [3, 6, 2], 11, 2
+        lens, q_lens = [23, 32, 9], [3, 6, 2]
+    B, N = 3, sum(new)
+    g = torch.Generator().manual_seed(9)
+    n_pages = 2 * B * width
+    lay = pkg.Layout([0], [d], [b], d, dR, 1, n_pages * page)
+    try:
+        lay.set_decode_path(path)
+        lay.arena[256:].random_(0, 256, generator=torch.Generator(device="cuda").manual_seed(1))
+        table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+        free, count = i32(list(range(n_pages))), i32([n_pages])
+        old = [_values(g, n, d, dR) for n in cached]
+        plan = lay.paged_plan(i32([0] * B), i32(cached), free, count, table, page, sum(cached))
+        lay.paged_write(0, torch.cat([c for c, _ in old]).cuda(), torch.cat([k for _, k in old]).cuda(),
+                        plan.slots)
+        assert lay.read_status() == 0
+        fresh = [_values(g, n, d, dR) for n in new]
+        plan = lay.paged_plan(i32(cached), i32(new), free, plan.free_count, table, page, max_new)
+        assert lay.read_status(clear=True) == pkg.KVK_FLAG_SEQ_LEN
+        # the caller's packed rows: all that it asked for; the map covers the first max_new
+        c, kr = torch.cat([c for c, _ in fresh]).cuda(), torch.cat([k for _, k in fresh]).cuda()
+        lay.paged_write(0, c[:max_new], kr[:max_new], plan.slots)
+        ql = torch.randn(N, H, d, generator=g).to(torch.bfloat16)
+        qr = torch.randn(N, H, dR, generator=g).to(torch.bfloat16)
+        out = torch.full((N, H, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((N, H), 7.0, device="cuda")
+        lay.mla_chunk(0, ql.cuda(), qr.cuda(), plan.q_start, plan.seq_lens, table, page, 0.07, out=out,
+                      lse=lse)
+        out, lse = out.cpu().double().numpy(), lse.cpu().double().numpy()
+        assert lay.read_status() == 0
+        assert plan.seq_lens.tolist() == lens
+        assert plan.q_start.tolist() == np.concatenate([[0], np.cumsum(q_lens)]).tolist()
+        q = torch.cat([ql.double(), qr.double()], 2).numpy()
+        row = 0
+        for i, (n, m) in enumerate(zip(lens, q_lens)):
+            if m == 0:
+                continue
+            rows, scale = dequantised(oracle_mod, torch.cat([old[i][0], fresh[i][0]])[:n],
+                                      torch.cat([old[i][1], fresh[i][1]])[:n], d, b, 0)
+            ref = chunk_reference(rows, q[row:row + m].reshape(m * H, -1),
+                                  np.repeat(n - m + np.arange(m) + 1, H), d, 0.07)
+            check_chunk(out[row:row + m].reshape(m * H, -1), lse[row:row + m].reshape(-1), ref,
+                        torch.bfloat16, b, 0, d + dR, n, rows, scale, d, path == 1, f"seq {i}")
+            row += m
+        assert (out[row:] == 7.0).all() and (lse[row:] == 7.0).all()
     finally:
         lay.close()
