@@ -173,7 +173,9 @@ kvk_status kvk_chunk_workspace_bytes(const kvk_layout* L, int layer, int n_q, in
       batch > kvk::kMaxPagedBatch || n_heads < 1 || n_heads > 4096)
     return KVK_ERR_INVALID_ARG;
   const AnchorDesc& A = L->anchors[L->slot[layer]];
-  *bytes = chunk_bytes(L, A, expand_pays(A.b, n_q, batch, n_heads), nullptr, nullptr);
+  // (bf16 queries take the tensor-core kernel wherever any do)
+  const bool expand = kvk::chunk_tc_supported(L, A, KVK_BF16) && expand_pays(A.b, n_q, batch, n_heads);
+  *bytes = chunk_bytes(L, A, expand, nullptr, nullptr);
   return KVK_OK;
 }
 

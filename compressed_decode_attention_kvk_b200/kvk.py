@@ -720,10 +720,36 @@ class Layout:
         return torch.empty(self.chunk_workspace_bytes(layer, n_q, batch, n_heads),
                            dtype=torch.uint8, device=self.arena.device)
 
+    def _scratch(self, nbytes):
+        return torch.empty(nbytes, dtype=torch.uint8, device=self.arena.device)
+
+    def _scratch_limit(self):
+        """Most bytes that a call allocates itself to expand a pool's rows: 1/8 of the GPU's memory."""
+        return torch.cuda.get_device_properties(self.arena.device).total_memory // 8
+
+    def _chunk_scratch(self, layer, dtype, n_q, batch, n_heads, page_tokens):
+        """The workspace of a chunk call that brings none.  Room for the expanded rows of the whole
+        pool (several times a 4-bit cache) is taken only where the call can use it, up to a limit,
+        and if the memory is there; without it the call converts the rows in the attention."""
+        base = self.chunk_workspace_bytes(layer, 0, batch, n_heads)
+        full = self.chunk_workspace_bytes(layer, n_q, batch, n_heads)
+        if full > base and page_tokens >= 8 and dtype in _DTYPE and full <= self._scratch_limit():
+            path = ctypes.c_int(0)
+            st = _lib_handle().kvk_chunk_path_for(self.handle, layer, _DTYPE[dtype],
+                                                  ctypes.byref(path))
+            if st == KVK_OK and path.value == KVK_PATH_TENSOR:
+                try:
+                    return self._scratch(full)
+                except torch.OutOfMemoryError:
+                    pass
+        return self._scratch(base)
+
     def mla_chunk(self, layer, q_lat, q_rope, q_start, seq_lens, block_table, page_tokens,
                   softmax_scale, out=None, lse=None, workspace=None, stream=None):
         """Causal attention of packed query rows over the paged cache (kvk_mla_chunk); returns
-        out [N, H, d] of the queries' dtype."""
+        out [N, H, d] of the queries' dtype.  Without a workspace each call allocates its own: the
+        size of new_chunk_workspace where the rows can be expanded, that is no more than 1/8 of the
+        GPU's memory, and it is free; the size for n_q = 0 otherwise."""
         N, H = q_lat.shape[:2]
         if not 0 <= layer < len(self.anchor):
             raise KvkError("kvk_mla_chunk", 1)
@@ -736,7 +762,7 @@ class Layout:
         if out is None:
             out = q_lat.new_empty((N, H, d))
         if workspace is None:
-            workspace = self.new_chunk_workspace(layer, N, seq_lens.numel(), H)
+            workspace = self._chunk_scratch(layer, q_lat.dtype, N, seq_lens.numel(), H, page_tokens)
         _mla_chunk(self.handle, layer, d, self.d_rope, q_lat, q_rope, q_start, seq_lens,
                    block_table, page_tokens, softmax_scale, out, workspace, lse, stream)
         return out

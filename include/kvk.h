@@ -490,9 +490,13 @@ kvk_status kvk_mla_chunk(kvk_layout* layout, int layer, const void* q_lat, const
 
 /* Bytes of device workspace for a kvk_mla_chunk of these sizes: partial results, a fixed size, and
  * from two tiles of 128 rows (query token, head) per sequence on (one over bf16 anchors) room for
- * the pool's rows expanded to 16-bit operands, up to 2 (d + d_rope) bytes a slot and twice that
- * for 16-bit or group-scaled codes.  A call that gets less than this, but no less than the size for
- * n_q = 0, converts the rows inside the attention, tile by tile; below that KVK_ERR_WORKSPACE. */
+ * the rows of the WHOLE pool expanded to 16-bit operands: per slot 2 (d' + d_rope') bytes, d' = d
+ * rounded up to 128 and d_rope' = d_rope to 64, twice that for 16-bit or group-scaled codes, and 4
+ * (a 4-bit pool of d = 512, d_rope = 64 takes 1156 bytes a slot so, four times its own 290).  Where
+ * the tensor-core kernel takes no query type (d > 512, d_rope > 64 or d_rope % 16) there are none.
+ * Calls over pages of fewer than 8 tokens and calls that take the CUDA-core kernel use the fixed
+ * part only.  A call that gets less than this, but no less than the size for n_q = 0, converts the
+ * rows inside the attention, tile by tile; below that KVK_ERR_WORKSPACE. */
 kvk_status kvk_chunk_workspace_bytes(const kvk_layout* layout, int layer, int n_q, int batch,
                                      int n_heads, size_t* bytes);
 

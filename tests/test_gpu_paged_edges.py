@@ -168,3 +168,34 @@ def test_an_overflowing_step_through_plan_write_and_attention(pkg, oracle_mod, k
         assert (out[row:] == 7.0).all() and (lse[row:] == 7.0).all()
     finally:
         lay.close()
+
+
+@pytest.mark.parametrize("short", ["limit", "memory"])
+def test_a_call_without_room_for_expanded_rows(pkg, oracle_mod, short):
+    """No workspace given, and the expanded rows of the pool beyond the limit or refused by the
+    allocator: the call converts the rows in the attention."""
+    q_lens, H = [60, 50], 12
+    pool = Pool(pkg, oracle_mod, [333, 200], 128, 64, 4, 0, 16, 8)
+    lay = pool.lay
+    try:
+        N = sum(q_lens)
+        base = lay.chunk_workspace_bytes(1, 0, 2, H)
+        assert lay.chunk_workspace_bytes(1, N, 2, H) > base
+        taken, make = [], lay._scratch
+
+        def scratch(n):
+            if n > base:
+                raise torch.OutOfMemoryError("test")
+            taken.append(n)
+            return make(n)
+        lay._scratch = scratch
+        if short == "limit":
+            lay._scratch_limit = lambda: base
+        ql, qr = pool.queries(q_lens, H, torch.bfloat16, 4)
+        lse = torch.empty(N, H, device="cuda")
+        out = lay.mla_chunk(1, ql.cuda(), qr.cuda(), i32([0, 60, 110]), i32(pool.lens),
+                            i32(pool.table.tolist()), pool.page, 0.07, lse=lse)
+        pool.check(q_lens, ql, qr, out.cpu(), lse.cpu(), torch.bfloat16, 0.07, True)
+        assert taken == [base] and lay.read_status() == 0
+    finally:
+        lay.close()

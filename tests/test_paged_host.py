@@ -101,3 +101,53 @@ def test_write_refuses_rows_narrower_than_the_layer(kvk, lay, through, width, ro
         write(torch.zeros(4, 64), torch.zeros(4, 16), slots)
     with pytest.raises(ValueError, match="CUDA"):
         write(torch.zeros(4, 80), torch.zeros(4, 24), slots)
+
+
+@pytest.mark.parametrize("d,dR,b,G", [(512, 64, 16, 0), (512, 64, 4, 0), (128, 64, 4, 32), (16, 16, 8, 0),
+                                      (192, 0, 0, 0), (528, 64, 8, 0), (512, 72, 8, 0), (512, 128, 8, 0)])
+def test_workspace_stays_within_its_documented_size(kvk, d, dR, b, G):
+    slots, batch, H = 3000, 4, 40
+    handle, _, _ = kvk.kvk_create_layout([0], [d], [b], d, dR, 1, slots, scale_group=G)
+    try:
+        base = kvk.kvk_chunk_workspace_bytes(handle, 0, 0, batch, H)
+        tile = -(-128 * batch // H)                 # query tokens of one row tile a sequence
+        small = kvk.kvk_chunk_workspace_bytes(handle, 0, tile - 1, batch, H)
+        large = kvk.kvk_chunk_workspace_bytes(handle, 0, 2 * tile, batch, H)
+        assert small == base
+        row = 2 * (-(-d // 128) * 128 + -(-dR // 64) * 64) * (2 if b == 16 or G else 1) + 4
+        tensor = d <= 512 and dR <= 64 and dR % 16 == 0
+        assert large - base == 0 if not tensor else slots * row <= large - base <= slots * row + 3 * 256
+    finally:
+        kvk.kvk_destroy(handle)
+
+
+@pytest.mark.parametrize("what,dtype,page,memory,want", [
+    ("fits", torch.bfloat16, 64, 10 ** 9, "full"),
+    ("fp32 queries", torch.float32, 64, 10 ** 9, "base"),
+    ("unknown queries", torch.float64, 64, 10 ** 9, "base"),
+    ("small pages", torch.bfloat16, 4, 10 ** 9, "base"),
+    ("no memory", torch.bfloat16, 64, 20 * 10 ** 6, "base"),
+    ("beyond the limit", torch.bfloat16, 64, 10 ** 12, "base"),
+])
+def test_a_call_without_workspace_takes_what_it_can_use(kvk, what, dtype, page, memory, want):
+    """The scratch that Layout.mla_chunk allocates itself: the expanded rows of the pool only where
+    the call expands rows, within the limit, and if the allocation succeeds."""
+    slots = 10 ** 6
+    lay = object.__new__(kvk.Layout)
+    lay.handle, _, _ = kvk.kvk_create_layout([0], [64], [8], 64, 16, 1, slots)
+    asked = []
+
+    def scratch(n):
+        asked.append(n)
+        if n > memory:
+            raise torch.OutOfMemoryError("test")
+        return n
+    lay._scratch = scratch
+    lay._scratch_limit = lambda: 10 ** 8 if what == "beyond the limit" else 10 ** 11
+    try:
+        sizes = {"base": lay.chunk_workspace_bytes(0, 0, 2, 8), "full": lay.chunk_workspace_bytes(0, 100, 2, 8)}
+        assert sizes["full"] - sizes["base"] > slots * 260
+        assert lay._chunk_scratch(0, dtype, 100, 2, 8, page) == sizes[want]
+        assert asked == ([sizes["full"], sizes["base"]] if what == "no memory" else [sizes[want]])
+    finally:
+        lay.close()
