@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(kHG * 32) chunk_fma_kernel(const __grid_consta
       }
       m = M;
     }
+    __syncwarp();                        // (the barrier wants whole warps)
     cluster_sync();                      // nobody's shared memory goes while it is read
     if (z) return;
   }

@@ -216,7 +216,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
       }
     }
   }
-  // every CTA has read the free count before it changes (one cluster, if it is updated in place)
+  // every CTA has read the free count before it changes (one cluster, if it is updated in place);
+  // the cluster's barrier wants whole warps, and the loops above leave theirs thread by thread
+  __syncthreads();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                ::: "memory");
   if (blockIdx.x == 0 && tid == 0)

@@ -7,7 +7,8 @@ import numpy as np
 import pytest
 import torch
 
-from paged_helpers import BF16_ROWS, check_chunk, chunk_reference, dequantised, random_table
+from paged_helpers import (BF16_ROWS, check_chunk, chunk_reference, dequantised, plan_reference,
+                           random_table)
 from test_gpu_paged import Pool, _run, _values, i32
 
 pytestmark = pytest.mark.gpu
@@ -106,6 +107,45 @@ def test_plan_keeps_the_first_max_new_tokens(pkg, batch, max_new):
             assert x == y, name
         over = sum(new) > max_new or any(a + f > width * page for a, f in zip(cached, new))
         assert lay.read_status(clear=True) == (pkg.KVK_FLAG_SEQ_LEN if over else 0)
+    finally:
+        lay.close()
+
+
+@pytest.mark.parametrize("in_place", [True, False], ids=["in_place", "apart"])
+@pytest.mark.parametrize("batch,most,max_new", [(7, 2500, 9000), (200, 190, 40000), (4096, 9, 40000),
+                                                (3, 100000, 300000)])
+def test_plan_by_many_ctas(pkg, batch, most, max_new, in_place):
+    """Plans that several CTAs share, the largest in grid strides (in place by a cluster of 8, else
+    by 64 CTAs), with the free count updated in place or apart; the slots of one call after the
+    other."""
+    rng = np.random.default_rng(batch)
+    page = 16
+    cached = rng.integers(0, 70, batch).tolist()
+    new = rng.integers(0, most, batch).tolist()
+    assert sum(new) <= max_new and sum(new) > max_new // 4
+    width = -(-(max(cached) + most) // page)
+    n_pages = sum(-(-(a + f) // page) for a, f in zip(cached, new)) + 5
+    table = random_table(rng, cached, page, n_pages, width)
+    held = set(table.ravel().tolist())
+    free = [int(p) for p in rng.permutation(n_pages) if p not in held]
+    ref = plan_reference(cached, new, free, len(free), table.tolist(), page, max_new, n_pages)
+    lay = pkg.Layout([0], [64], [4], 64, 16, 1, n_pages * page)
+    try:
+        c, f, fp = i32(cached), i32(new), i32(free)
+        for rep in range(5):
+            t, count = i32(table.tolist()), i32([len(free)])
+            out = lay.new_paged_plan(batch, max_new)
+            out = out._replace(free_count=count) if in_place else out
+            for x in out:
+                if x is not count:
+                    x.fill_(-77)
+            p = lay.paged_plan(c, f, fp, count, t, page, max_new, out=out)
+            got = (t.tolist(), p.seq_lens.tolist(), p.q_start.tolist(), p.slots.tolist(),
+                   p.positions.tolist(), p.free_count.item())
+            for name, x, y in zip(("table", "seq_lens", "q_start", "slots", "positions", "free"), got, ref):
+                assert x == y, (name, rep)
+            assert in_place or int(count) == len(free)
+        assert lay.read_status() == 0
     finally:
         lay.close()
 
