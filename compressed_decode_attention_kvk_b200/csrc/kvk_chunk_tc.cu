@@ -47,8 +47,11 @@
 //
 // Softmax with token scales.  With z_t the score in log2 units and s_t the token's scale, the
 // weight of code row t is s_t 2^(z_t): the kernel tracks w_t = z_t + log2 s_t, m >= max w_t - 8,
-// P_t = 2^(w_t - m) and l = sum P_t / s_t, so that P fits 16 bits whatever the scales.  A token
-// that does not exist (behind the end, or on a page outside the pool) has log2 s_t = -inf.
+// P_t = 2^(w_t - m + 7) and l = sum P_t / s_t, so that P fits 16 bits whatever the scales: at most
+// 2^15, the largest at least 2^7.  f16 holds weights down to 2^-25 of 1 (half its smallest step):
+// 2^-32 of the largest, of which a sum of 2^20 such tokens loses 2^-12 at most; l, in fp32, counts
+// them all.  A token that does not exist (behind the end, or on a page outside the pool) has
+// log2 s_t = -inf.
 //
 // Measured on one B200 (us, with expansion and merge; of the measured bf16 rate or copy bandwidth):
 // 1024 rows x 40 heads over 32768 bf16 tokens, d = 512: 2341 (0.74); 4 x 512 rows near 8192 tokens
@@ -83,6 +86,8 @@ constexpr uint32_t kSCol = 256;        // S buffers at 256 and 320 (64 columns);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;          // growth of a row's maximum that its reference lets pass
+constexpr float kHead = 7.0f;          // weights are held times 2^7 (below)
+static_assert(kLazy + kHead <= 15.0f, "a weight fits f16");
 constexpr int kSmemLimit = 232448;
 constexpr int kMaxK = 8;               // slots of the K ring, two atoms each
 constexpr int kStep = 2;               // atoms of a K ring slot
@@ -1328,7 +1333,7 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
         l *= alpha;
         m = mx;
       }
-      const float mref = m == -CUDART_INF_F ? 0.0f : m;
+      const float mref = m == -CUDART_INF_F ? 0.0f : m - kHead;
       // The previous output MMA has to have read P and left O before this block's P is written.
       // Waited for ahead of the exponentials, but over bf16 rows (one score MMA a block, softmax
       // the longer side) behind the first of them; us ahead / behind, expanded rows, d = 512: 8
@@ -1417,11 +1422,11 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
       write_o(obase, ocg, f0, row_ok ? a.d : 0, to, dest >= 0 ? -1 : P.q_bf16, inv);
       if (hh == 0 && cg == 0 && row_ok) {
         if (dest >= 0) {
-          P.w.ml[2 * (int64_t)part] = m;
+          P.w.ml[2 * (int64_t)part] = m - kHead;
           P.w.ml[2 * (int64_t)part + 1] = lt;
         } else if (a.lse) {
           a.lse[(int64_t)row_q * a.H + row_h] =
-              lt == 0.0f ? -CUDART_INF_F : kLn2 * (m + log2f(lt));
+              lt == 0.0f ? -CUDART_INF_F : kLn2 * (m - kHead + log2f(lt));
         }
       }
       if (dest >= 0 && rank == 0 && tid == 0) {

@@ -239,3 +239,130 @@ def test_a_call_without_room_for_expanded_rows(pkg, oracle_mod, short):
         assert taken == [base] and lay.read_status() == 0
     finally:
         lay.close()
+
+
+# ---------------------------------------------------------------------------------------
+# weights of very different size
+# ---------------------------------------------------------------------------------------
+
+HALF16 = 2.0 ** -11
+
+
+def _weighted_check(rows, scale, q, limits, d, sigma, out, lse, b, G, what):
+    """Elementwise bound that counts the tensor-core kernel's roundings (see check_chunk), with f16's
+    subnormals as they are: P_t is off by at most 2^-25, the largest P is at least 2^7, and P_t / l
+    is s_t p_t (with group scales and bf16 rows p_t), so that a row's output is off by at most
+    2^-32 max_t(s_t p_t) sum_t |code_t|."""
+    n, T = rows.shape[1], len(rows)
+    seen = np.arange(T)[None, :] < np.asarray(limits)[:, None]
+    z = np.where(seen, (q @ rows.T) * sigma, -np.inf)
+    m = z.max(1, keepdims=True)
+    p = np.exp(z - m)
+    l = p.sum(1, keepdims=True)
+    p /= l
+    ref = p @ rows[:, :d]
+    unit = np.where(seen, (np.abs(q) @ np.abs(rows).T) * abs(sigma), 0.0).max(1, keepdims=True)
+    rel = 2 * (n + 4) * 2.0 ** -24 * unit + 2 * T * 2.0 ** -24 + 2.0 ** -20 + HALF16
+    if b == 16 or G:
+        rel = rel + HALF16
+    s = np.ones((T, 1)) if G else np.where(scale[:, :1] > 0, scale[:, :1], 1.0)
+    # (in place of a scale of 0 the kernel takes 2^-24, f16's least)
+    held = s if G else np.where(scale[:, :1] > 0, scale[:, :1], 2.0 ** -24)
+    top = (p * held[:, 0]).max(1, keepdims=True)
+    codes = np.abs(rows[:, :d]) / s
+    sub = 2.0 ** -32 * top * (seen.astype(np.float64) @ codes)
+    tol = (rel * (p @ np.abs(rows[:, :d])) + sub) * (1 + 2.0 ** -6) + np.abs(ref) * 2.0 ** -8 * 1.01 + 1e-30
+    assert np.isfinite(out).all()
+    worst = (np.abs(out - ref) / tol).max()
+    assert worst <= 1.0, f"{what}: {worst:.2f} x the bound"
+    le = (m + np.log(l))[:, 0]
+    tl = (2 * (n + 4) * 2.0 ** -24 * unit + 2 * T * 2.0 ** -24 + 1e-5)[:, 0] + 2.0 ** -22 * np.abs(le)
+    assert (np.abs(lse - le) <= tl).all(), f"{what}: lse"
+
+
+def _attend(pkg, c, kr, d, b, G, ql, qr, sigma, path):
+    T, N, H = len(c), ql.shape[0], ql.shape[1]
+    lay = pkg.Layout([0], [d], [b], d, kr.shape[1], 1, -(-T // 64) * 64, scale_group=G)
+    try:
+        lay.paged_write(0, c.cuda(), kr.cuda(), torch.arange(T, dtype=torch.int32, device="cuda"))
+        lay.set_decode_path(path)
+        lse = torch.empty(N, H, device="cuda")
+        out = lay.mla_chunk(0, ql.cuda(), qr.cuda(), i32([0, N]), i32([T]),
+                            i32([list(range(-(-T // 64)))]), 64, sigma, lse=lse)
+        assert lay.read_status() == 0
+        return out.cpu().double().numpy().reshape(N * H, -1), lse.cpu().double().numpy().reshape(-1)
+    finally:
+        lay.close()
+
+
+@pytest.mark.parametrize("q_len", [1, 16], ids=["one", "expanded"])
+@pytest.mark.parametrize("gap", [12, 18, 24])
+@pytest.mark.parametrize("b,G", [(8, 0), (16, 0), (4, 32), (2, 0)])
+def test_many_small_weights_beside_a_large_one(pkg, oracle_mod, b, G, gap, q_len):
+    """One token whose score is 2^gap times every other's weight and whose latents are zero: the
+    output is made of the small weights alone, which must not vanish beside it."""
+    d, dR, T, H, big = 128, 64, 5000, 20, 77
+    g = torch.Generator().manual_seed(gap)
+    c = (torch.rand(T, d, generator=g) + 0.5).to(torch.bfloat16)
+    kr = torch.zeros(T, dR, dtype=torch.bfloat16)
+    c[big] = 0
+    kr[big, :32] = 2.0
+    ql = torch.zeros(q_len, H, d, dtype=torch.bfloat16)
+    qr = torch.zeros(q_len, H, dR, dtype=torch.bfloat16)
+    qr[..., :32] = 1.0
+    sigma = gap * math.log(2.0) / 64.0               # the large token's score: gap powers of two
+    rows, scale = dequantised(oracle_mod, c, kr, d, b, G)
+    q = torch.cat([ql.double(), qr.double()], 2).numpy().reshape(q_len * H, -1)
+    lim = np.repeat(T - q_len + np.arange(q_len) + 1, H)
+    out, lse = _attend(pkg, c, kr, d, b, G, ql, qr, sigma, pkg.KVK_PATH_TENSOR)
+    _weighted_check(rows, scale, q, lim, d, sigma, out, lse, b, G, f"gap {gap}")
+
+
+@pytest.mark.parametrize("q_len", [1, 3, 16])
+@pytest.mark.parametrize("d", [64, 512])
+@pytest.mark.parametrize("b", [2, 4, 8, 16])
+def test_token_scales_far_apart_and_zero(pkg, oracle_mod, b, d, q_len):
+    """Tokens of magnitudes from 2^-9 to 2^6 side by side, and tokens that are zero altogether (their
+    score is 0, their scale too)."""
+    dR, T, H = 64, 600, 20
+    g = torch.Generator().manual_seed(b + d)
+    mag = torch.exp2(torch.randint(-9, 7, (T, 1), generator=g).float())
+    c = (torch.randn(T, d, generator=g) * mag).to(torch.bfloat16)
+    kr = (torch.randn(T, dR, generator=g) * mag).to(torch.bfloat16)
+    for t in (0, 5, 127, 128, 300, 598):
+        c[t], kr[t] = 0, 0
+    ql = torch.randn(q_len, H, d, generator=g).to(torch.bfloat16)
+    qr = torch.randn(q_len, H, dR, generator=g).to(torch.bfloat16)
+    sigma = 0.02 / math.sqrt(d / 64)
+    rows, scale = dequantised(oracle_mod, c, kr, d, b, 0)
+    assert (scale[:, 0] == 0).sum() == 6 and scale.max() / scale[scale > 0].min() > 2 ** 12
+    q = torch.cat([ql.double(), qr.double()], 2).numpy().reshape(q_len * H, -1)
+    lim = np.repeat(T - q_len + np.arange(q_len) + 1, H)
+    for path in (pkg.KVK_PATH_TENSOR, pkg.KVK_PATH_CUDA_CORE):
+        out, lse = _attend(pkg, c, kr, d, b, 0, ql, qr, sigma, path)
+        _weighted_check(rows, scale, q, lim, d, sigma, out, lse, b, 0, f"path {path}")
+
+
+@pytest.mark.parametrize("value", [0.0, 1.0])
+def test_a_cache_of_equal_tokens(pkg, oracle_mod, value):
+    """All tokens zero, or all the same: every weight is equal, lse is the logarithm of their count."""
+    d, dR, T, H = 128, 64, 300, 8
+    c, kr = torch.full((T, d), value), torch.full((T, dR), value)
+    g = torch.Generator().manual_seed(1)
+    for b, G in ((8, 0), (16, 0), (4, 32), (BF16_ROWS, 0)):
+        for q_len in (1, 40):
+            ql = torch.randn(q_len, H, d, generator=g).to(torch.bfloat16)
+            qr = torch.randn(q_len, H, dR, generator=g).to(torch.bfloat16)
+            for path in (pkg.KVK_PATH_TENSOR, pkg.KVK_PATH_CUDA_CORE):
+                out, lse = _attend(pkg, c, kr, d, b, G, ql, qr, 0.05, path)
+                rows, _ = dequantised(oracle_mod, c, kr, d, b, G)
+                q = torch.cat([ql.double(), qr.double()], 2).numpy()
+                z = (q @ rows[0]) * 0.05
+                n = T - q_len + np.arange(q_len) + 1
+                le = (z + np.log(n)[:, None]).reshape(-1)
+                # the mean of equal values: the rows' high part, P (the same for all tokens), the
+                # sums of T terms, the output's half step
+                step = 2.0 ** -11 + 2.0 ** -8 + 2 * T * 2.0 ** -24 + 2.0 ** -8 * 1.01
+                assert np.abs(out - rows[0, :d]).max() <= np.abs(rows[0, :d]).max() * step
+                dz = (d + dR + 4) * 2.0 ** -24 * (np.abs(q) @ np.abs(rows[0])).max() * 0.05
+                assert np.abs(lse - le).max() <= 2 * dz + 2 * T * 2.0 ** -24 + 1e-5
