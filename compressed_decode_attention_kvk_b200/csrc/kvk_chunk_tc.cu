@@ -65,6 +65,7 @@
 #include <algorithm>
 
 #include "kvk_chunk_convert.cuh"
+#include "kvk_chunk_route.cuh"
 #include "kvk_chunk_stop.cuh"
 #include "kvk_chunk_tc.cuh"
 #include "kvk_decode_common.cuh"
@@ -93,7 +94,8 @@ constexpr int kMaxK = 8;               // slots of the K ring, two atoms each
 constexpr int kStep = 2;               // atoms of a K ring slot
 constexpr uint64_t kDrainLimitNs = 2000000000ull;
 
-constexpr uint32_t kLaunchRegs = 65536 / kThreads;
+constexpr uint32_t kLaunchRegs = kChunkLaunchRegs;
+static_assert(kLaunchRegs * kThreads == 65536, "one block takes the SM's registers");
 template <uint32_t N>
 __device__ __forceinline__ void regs_set() {
   if constexpr (N > kLaunchRegs) regs_inc<N>();
@@ -1606,17 +1608,34 @@ bool expanded_map(CUtensorMap* m, void* base, int NA, int64_t slots, int rows) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Registers a thread of an instance (0 where the device does not tell; asked again then).
+template <int BITS, bool GROUP, bool kExp>
+int instance_regs() {
+  static std::atomic<int> regs{0};
+  int r = regs.load(std::memory_order_relaxed);
+  if (r) return r;
+  cudaFuncAttributes at;
+  if (cudaFuncGetAttributes(&at, chunk_tc_kernel<BITS, GROUP, kExp>) == cudaSuccess) r = at.numRegs;
+  else cudaGetLastError();
+  regs.store(r, std::memory_order_relaxed);
+  return r;
+}
+// Of the converting instance for rows of BITS and the expanded one that they share with others.
+template <int BITS, int EXP_BITS, bool GROUP>
+int both_regs() {
+  const int r = instance_regs<BITS, GROUP, false>();
+  return r == instance_regs<EXP_BITS, GROUP, true>() ? r : 0;
+}
+
 template <int BITS, bool GROUP, bool kExp>
 cudaError_t launch(const TcChunk& P, const CUtensorMap& hi, const CUtensorMap& lo, size_t smem,
                    cudaStream_t st) {
   auto k = chunk_tc_kernel<BITS, GROUP, kExp>;
   // the kernel hands registers from warpgroup to warpgroup: their number at launch is part of it
+  // (the caller has chosen its path by it)
+  if (instance_regs<BITS, GROUP, kExp>() != (int)kLaunchRegs) return cudaErrorNotSupported;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = once_per_device(done, [&] {
-    cudaFuncAttributes at;
-    const cudaError_t r = cudaFuncGetAttributes(&at, k);
-    if (r != cudaSuccess) return r;
-    if (at.numRegs != (int)kLaunchRegs) return cudaErrorNotSupported;
     return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   });
   if (e != cudaSuccess) return e;
@@ -1631,6 +1650,20 @@ bool chunk_tc_supported(const kvk_layout* L, const AnchorDesc& A, int dtype) {
   // bf16 rows stay bf16 in the MMA, whose two operands have one type
   if (A.b == KVK_BITS_BF16 && dtype != KVK_BF16) return false;
   return A.d <= 512 && L->d_rope <= 64 && L->d_rope % 16 == 0;
+}
+
+int chunk_tc_regs(int b, int group) {
+  if (group) {
+    if (b == 2) return both_regs<2, 8, true>();
+    if (b == 4) return both_regs<4, 8, true>();
+    if (b == 8) return both_regs<8, 8, true>();
+    return both_regs<16, 8, true>();
+  }
+  if (b == KVK_BITS_BF16) return both_regs<KVK_BITS_BF16, KVK_BITS_BF16, false>();
+  if (b == 2) return both_regs<2, 8, false>();
+  if (b == 4) return both_regs<4, 8, false>();
+  if (b == 8) return both_regs<8, 8, false>();
+  return both_regs<16, 16, false>();
 }
 
 cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkWork& w, int dtype, cudaStream_t st) {

@@ -37,6 +37,9 @@ size_t chunk_workspace(const AnchorDesc& A, int d_rope, int group, int64_t slots
 // Expands the rows of every sequence that has queries (kvk_chunk_expand.cu).
 cudaError_t launch_chunk_expand(const ChunkArgs& a, const ChunkWork& w, cudaStream_t st);
 bool chunk_tc_supported(const kvk_layout* L, const AnchorDesc& A, int dtype);
+// Registers a thread that the kernel's two instances for these rows (converting, expanded) were
+// built with; 0 where they differ, or the device does not tell.
+int chunk_tc_regs(int b, int group);
 cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkWork& w, int dtype, cudaStream_t st);
 
 // two outputs as one 32-bit word of bf16 or f16

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 
+#include "kvk_chunk_route.cuh"
 #include "kvk_chunk_tc.cuh"
 
 using kvk::AnchorDesc;
@@ -36,12 +37,11 @@ int chunk_clusters(const kvk_layout* L) {
   return std::max(1, (L->num_sms > 0 ? L->num_sms : 148) / 2);
 }
 
-// The kernel a chunk call takes, or -1: the tensor-core kernel where it applies (bf16 and f16
-// queries), the CUDA-core kernel otherwise, as the layout's decode path allows.
+// The kernel a chunk call takes, or -1 (bf16 and f16 queries may take the tensor-core kernel).
 int chunk_path(const kvk_layout* L, const AnchorDesc& A, int dtype) {
-  if (L->path != KVK_PATH_CUDA_CORE && kvk::chunk_tc_supported(L, A, dtype)) return KVK_PATH_TENSOR;
-  if (L->path == KVK_PATH_TENSOR || L->path == KVK_PATH_TENSOR_GENERAL) return -1;
-  return kvk::chunk_fma_fits(A.n) ? KVK_PATH_CUDA_CORE : -1;
+  const bool tensor = kvk::chunk_tc_supported(L, A, dtype);
+  const int regs = tensor && L->arena ? kvk::chunk_tc_regs(A.b, kvk::anchor_group(L, A)) : -1;
+  return kvk::chunk_route(L->path, tensor, regs, kvk::chunk_fma_fits(A.n));
 }
 
 // Whether a call's rows are converted once ahead of the attention (kvk_chunk_expand.cu) instead
