@@ -79,3 +79,27 @@ def test_traffic_record_follows_kernel_code_not_comments(tmp_path):
         assert bench.decode_traffic() is not None
     else:
         assert bench.decode_traffic() is None
+
+
+def test_traffic_record_does_not_depend_on_entry_points(tmp_path):
+    """A new entry point in the header leaves the kernel's hash, and with it the record, alone; a
+    changed constant does not."""
+    import shutil
+    import bench
+    for rel in bench.KERNEL_SOURCES:
+        dst = tmp_path / rel
+        dst.parent.mkdir(parents=True, exist_ok=True)
+        shutil.copy(os.path.join(ROOT, rel), dst)
+    base = bench.kernel_code_hash(str(tmp_path))
+    h = tmp_path / "include/kvk.h"
+    src = h.read_text()
+    assert "#define KVK_PATH_TENSOR " in src
+    h.write_text(src.replace("#endif", "kvk_status kvk_another(kvk_layout* layout);\n#endif", 1))
+    assert bench.kernel_code_hash(str(tmp_path)) == base
+    h.write_text(src.replace("#define KVK_PATH_TENSOR ", "#define KVK_PATH_TENSOR 9", 1))
+    assert bench.kernel_code_hash(str(tmp_path)) != base
+    # the record's ratio is that of its own figures
+    rec = json.load(open(os.path.join(ROOT, "profiles", "decode_tc_traffic.json")))
+    for r in (rec, rec["b8_same_kernel"]):
+        moved = r["dram_read_bytes"] + r["dram_write_bytes"]
+        assert abs(moved / r["algorithmic_bytes"] - r["dram_over_algorithmic"]) < 1e-4
