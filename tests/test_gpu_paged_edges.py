@@ -366,3 +366,133 @@ def test_a_cache_of_equal_tokens(pkg, oracle_mod, value):
                 assert np.abs(out - rows[0, :d]).max() <= np.abs(rows[0, :d]).max() * step
                 dz = (d + dR + 4) * 2.0 ** -24 * (np.abs(q) @ np.abs(rows[0])).max() * 0.05
                 assert np.abs(lse - le).max() <= 2 * dz + 2 * T * 2.0 ** -24 + 1e-5
+
+
+# ---------------------------------------------------------------------------------------
+# group scales, and the contiguous calls beside the paged ones
+# ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("q_lens", [[3, 1], [70, 90]], ids=["few", "expanded"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("b,G", [(16, 32), (8, 64), (4, 32), (2, 16)])
+@pytest.mark.parametrize("d,dR", [(512, 64), (384, 64), (256, 64), (64, 32)])
+def test_group_scales_at_every_rank(pkg, oracle_mod, d, dR, b, G, dtype, q_lens):
+    """Group-scaled rows under bf16 and f16 queries at the ranks whose rings and stages differ."""
+    if (d + dR) % G:
+        pytest.skip("the group does not divide the row")
+    lens, H = [333, 260], 9
+    pool = Pool(pkg, oracle_mod, lens, d, dR, b, G, 32, d + b + G)
+    try:
+        assert pool.lay.chunk_path_for(0, dtype) == pkg.KVK_PATH_TENSOR
+        sigma = 1 / math.sqrt(d + dR)
+        ql, qr = pool.queries(q_lens, H, dtype, 7, gain=1.5)
+        for path in (pkg.KVK_PATH_TENSOR, pkg.KVK_PATH_CUDA_CORE):
+            out, lse = _run(pool, pkg, path, q_lens, ql, qr, sigma, dtype)
+            q = torch.cat([ql.double(), qr.double()], 2).numpy()
+            row = 0
+            for i, (n, m) in enumerate(zip(lens, q_lens)):
+                ref = chunk_reference(pool.rows[i], q[row:row + m].reshape(m * H, -1),
+                                      np.repeat(n - m + np.arange(m) + 1, H), d, sigma)
+                o = out[row:row + m].double().numpy().reshape(m * H, -1)
+                if dtype == torch.float16:
+                    # an f16 below 2^-14 has steps of 2^-24, whatever its value: its rounding is off by
+                    # up to 2^-25 (a feature that only tokens of weight 3e-8 hold: -3.5e-8 rounds to
+                    # -6.0e-8), which the half step relative to the value does not count
+                    e = o - ref[0]
+                    o = ref[0] + np.sign(e) * np.maximum(np.abs(e) - 2.0 ** -25, 0.0)
+                check_chunk(o, lse[row:row + m].double().numpy().reshape(-1), ref, dtype, b, G, d + dR, n,
+                            pool.rows[i], pool.scale[i], d, path == pkg.KVK_PATH_TENSOR,
+                            f"path {path} seq {i}")
+                row += m
+        assert pool.lay.read_status() == 0
+    finally:
+        pool.lay.close()
+
+
+@pytest.mark.parametrize("b,G", [(8, 0), (16, 0), (4, 32), (BF16_ROWS, 0)])
+def test_decode_steps_beside_the_contiguous_calls(pkg, oracle_mod, b, G):
+    """A prompt and then one-token steps, through plan, write and chunk attention and through
+    kvk_quant_write and kvk_mla_decode over a contiguous cache: both within their bounds of the fp64
+    form, and of one another."""
+    d, dR, H, page, steps = 256, 64, 12, 16, 6
+    prompt = [45, 130, 7]
+    B, top = len(prompt), max(prompt) + steps
+    g = torch.Generator().manual_seed(b + 6)
+    c = [_values(g, n + steps, d, dR) for n in prompt]
+    n_pages = sum(-(-(n + steps) // page) for n in prompt) + 2
+    paged = pkg.Layout([0], [d], [b], d, dR, 1, n_pages * page, scale_group=G)
+    flat = pkg.Layout([0], [d], [b], d, dR, B, top, scale_group=G)
+    sigma = 1 / math.sqrt(d + dR)
+    try:
+        table = torch.full((B, -(-top // page)), -1, dtype=torch.int32, device="cuda")
+        free, count = i32(list(range(n_pages))), i32([n_pages])
+        cached, done = i32([0] * B), [0] * B
+        for step in range(steps + 1):
+            new = prompt if step == 0 else [1] * B
+            N = sum(new)
+            cs = [c[i][0][done[i]:done[i] + new[i]] for i in range(B)]
+            ks = [c[i][1][done[i]:done[i] + new[i]] for i in range(B)]
+            plan = paged.paged_plan(cached, i32(new), free, count, table, page, N)
+            paged.paged_write(0, torch.cat(cs).cuda(), torch.cat(ks).cuda(), plan.slots)
+            wide = max(new)                          # (rows behind a prompt's end lie past the cache)
+            cf, kf = torch.zeros(B, wide, d, dtype=cs[0].dtype), torch.zeros(B, wide, dR, dtype=cs[0].dtype)
+            for i in range(B):
+                cf[i, :new[i]], kf[i, :new[i]] = cs[i], ks[i]
+            flat.quant_write(0, cf.cuda(), kf.cuda(), cached)
+            flat.read_status(clear=True)             # (and are flagged as such)
+            done = [a + n for a, n in zip(done, new)]
+            cached, count = plan.seq_lens, plan.free_count
+            if step == 0:
+                continue
+            ql = torch.randn(B, H, d, generator=g).to(torch.bfloat16)
+            qr = torch.randn(B, H, dR, generator=g).to(torch.bfloat16)
+            lse, lse_flat = torch.empty(B, H, device="cuda"), torch.empty(B, H, device="cuda")
+            out = paged.mla_chunk(0, ql.cuda(), qr.cuda(), plan.q_start, plan.seq_lens, table, page, sigma,
+                                  lse=lse).cpu().double().numpy()
+            out_flat = flat.mla_decode(0, ql.cuda(), qr.cuda(), plan.seq_lens, sigma,
+                                       lse=lse_flat).cpu().double().numpy()
+            lse, lse_flat = lse.cpu().double().numpy(), lse_flat.cpu().double().numpy()
+            for i, n in enumerate(done):
+                rows, scale = dequantised(oracle_mod, c[i][0][:n], c[i][1][:n], d, b, G)
+                q = torch.cat([ql[i].double(), qr[i].double()], 1).numpy()
+                ref = chunk_reference(rows, q, [n] * H, d, sigma)
+                args = (b, G, d + dR, n, rows, scale, d, True)
+                check_chunk(out[i], lse[i], ref, torch.bfloat16, *args, f"paged, step {step} seq {i}")
+                check_chunk(out_flat[i], lse_flat[i], ref, torch.float32, *args, f"flat, step {step} seq {i}")
+                dz = ((d + dR + 4) * 2.0 ** -24 * ref[3])[:, None]
+                rel = 2 * dz + 2 * n * 2.0 ** -24 + 2.0 ** -20 + (2.0 ** -8 if b == BF16_ROWS else 2.0 ** -10)
+                tol = 2 * rel * ref[2] * (1 + 2.0 ** -6) + np.abs(ref[0]) * 2.0 ** -8 * 1.02 + 1e-6
+                assert (np.abs(out[i] - out_flat[i]) <= tol).all()
+                assert (np.abs(lse[i] - lse_flat[i]) <= 4 * dz[:, 0] + 4 * n * 2.0 ** -24 + 2e-5).all()
+        assert paged.read_status() == 0 and flat.read_status() == 0
+    finally:
+        paged.close()
+        flat.close()
+
+
+@pytest.mark.parametrize("b,G,d,H,q_lens", [(16, 0, 512, 40, [1] * 6), (8, 0, 512, 20, [90, 3, 1, 64, 0, 70]),
+                                            (4, 32, 128, 40, [40] * 6), (BF16_ROWS, 0, 384, 24, [33] * 6)])
+def test_calls_repeat_to_the_bit(pkg, oracle_mod, b, G, d, H, q_lens):
+    """The work is split and joined by the lengths alone: the same call gives the same bits, also over
+    a workspace that another call has used."""
+    lens = [900, 300, 1, 640, 50, 2000]
+    pool = Pool(pkg, oracle_mod, lens, d, 64, b, G, 64, 4)
+    try:
+        q_lens = [min(a, n) for a, n in zip(q_lens, lens)]
+        N = sum(q_lens)
+        ql, qr = pool.queries(q_lens, H, torch.bfloat16, 2)
+        args = (ql.cuda(), qr.cuda(), i32(np.concatenate([[0], np.cumsum(q_lens)]).tolist()), i32(lens),
+                i32(pool.table.tolist()), 64, 0.05)
+        ws = pool.lay.new_chunk_workspace(0, N, len(lens), H)
+        first = None
+        for rep in range(8):
+            if rep % 2:                              # the workspace's contents of a call of other sizes
+                pool.lay.mla_chunk(0, args[0][:1], args[1][:1], i32([0] * 5 + [0, 1]), *args[3:], workspace=ws)
+            lse = torch.empty(N, H, device="cuda")
+            out = pool.lay.mla_chunk(0, *args, lse=lse, workspace=ws)
+            if first is None:
+                first = (out, lse)
+            assert torch.equal(out, first[0]) and torch.equal(lse, first[1]), rep
+        pool.check(q_lens, ql, qr, first[0].cpu(), first[1].cpu(), torch.bfloat16, 0.05, True)
+    finally:
+        pool.lay.close()
