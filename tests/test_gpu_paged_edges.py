@@ -496,3 +496,24 @@ def test_calls_repeat_to_the_bit(pkg, oracle_mod, b, G, d, H, q_lens):
         pool.check(q_lens, ql, qr, first[0].cpu(), first[1].cpu(), torch.bfloat16, 0.05, True)
     finally:
         pool.lay.close()
+
+
+@pytest.mark.parametrize("d,dR,b,G", [(528, 64, 8, 0), (1024, 64, 16, 0), (2032, 16, 4, 0), (1024, 64, 4, 32),
+                                      (2048, 0, BF16_ROWS, 0), (128, 72, 8, 0), (128, 8, 2, 0), (48, 128, 16, 0),
+                                      (512, 8, 4, 0)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_widths_of_the_cuda_core_kernel_only(pkg, oracle_mod, d, dR, b, G, dtype):
+    """Ranks beyond 512 and RoPE widths that the tensor-core kernel does not take, from one query token
+    (a cluster splits the keys) to many."""
+    lens, H = [150, 70], 9
+    pool = Pool(pkg, oracle_mod, lens, d, dR, b, G, 16, d + b)
+    try:
+        assert pool.lay.chunk_path_for(0, dtype) == pkg.KVK_PATH_CUDA_CORE
+        sigma = 1 / math.sqrt(d + dR)
+        for q_lens in ([1, 0], [2, 1], [40, 30]):
+            ql, qr = pool.queries(q_lens, H, dtype, 7, gain=1.5)
+            out, lse = _run(pool, pkg, pkg.KVK_PATH_AUTO, q_lens, ql, qr, sigma, dtype)
+            pool.check(q_lens, ql, qr, out, lse, dtype, sigma, False, f"{q_lens}")
+        assert pool.lay.read_status() == 0
+    finally:
+        pool.lay.close()
