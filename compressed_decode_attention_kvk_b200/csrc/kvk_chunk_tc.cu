@@ -40,7 +40,11 @@
 // Numbers.  Codes enter the MMA exactly: a code of at most 8 bits is an f16 integer; a 16-bit
 // code c and a group-scaled value c s are split into two f16 parts (hi = f16(x), lo = x - hi)
 // whose score MMAs add up.  The output MMA takes the high part (at most 2^-11 of the value) and P
-// in f16 (2^-11); bf16 rows stay bf16, P too (2^-8, as the rows' own rounding).  A bf16 query is
+// in f16 (2^-11): with bf16 outputs (2^-8) neither shows, with f16 outputs (2^-11) the error against
+// 64 bits is 2.3e-4 where rounding the output alone gives 2.1e-4.  bf16 rows stay bf16, since f16
+// lacks their range and both operands of an MMA have one type; P is then bf16 too (2^-8, the outputs'
+// and the rows' own rounding), where the contiguous decode converts such rows and keeps P in f16.  A
+// weight's low part would take a second output MMA.  A bf16 query is
 // scaled by a power of two of its row into f16's range: exact but for elements far below the
 // row's largest, which f16's subnormals leave off by at most 2^-39 of it.
 // Scores, references and sums are fp32.
@@ -54,10 +58,11 @@
 // log2 s_t = -inf.
 //
 // Measured on one B200 (us, with expansion and merge; of the measured bf16 rate or copy bandwidth):
-// 1024 rows x 40 heads over 32768 bf16 tokens, d = 512: 2341 (0.74); 4 x 512 rows near 8192 tokens
-// of 8 bits: 1323 (0.62); 8 ragged chunks over 4-bit groups, d = 128: 315 (0.29, two score MMAs);
-// decode of 32 x 8192 16-bit tokens, 40 heads: 219 (0.21 of the bandwidth).  Counters of the last
-// three: tensor pipe active 57, 40 and 25 %, 1.2 to 1.8 instructions a cycle, no pipe full: the
+// 1024 rows x 40 heads over 32768 bf16 tokens, d = 512: 2371 (0.73); 4 x 512 rows near 8192 tokens
+// of 8 bits: 1357 (0.60); 16 ragged sequences with 4 to 301 new tokens, 16 bits, d = 384: 741
+// (0.31, two score MMAs); 8 ragged chunks over 4-bit groups, d = 128: 320 (0.28, two score MMAs);
+// decode of 32 x 8192 16-bit tokens, 40 heads: 221 (0.21 of the bandwidth).  Counters of the last
+// four: tensor pipe active 57, 48, 40 and 25 %, 1.1 to 1.8 instructions a cycle, no pipe full: the
 // hand-overs of a block (rows landed, scores done, weights written, output free) bound it.
 #include <math_constants.h>
 #include <string.h>
@@ -526,10 +531,6 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
   TokRing ring(P.NT);
   Shared& S = *reinterpret_cast<Shared*>(smem + P.off_misc);
   const uint32_t q_s = smem_u32(smem), k_s = q_s + P.off_k, v_s = q_s + P.off_v, p_s = q_s + P.off_p;
-  // The warp index, and what a warp reads from shared memory to steer its MMAs, go through a
-  // shuffle: known to be the same in every lane, they and all that follows from them stay in
-  // uniform registers, where the MMA's operands have to be.  (A block's MMAs with their waits and
-  // commits: 2264 cycles issued so, 4545 from per-lane registers.)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cta_rank();
   const int cluster = blockIdx.x >> 1;
@@ -672,8 +673,9 @@ chunk_tc_kernel(const __grid_constant__ TcChunk P, const __grid_constant__ CUten
   const int nch = (P.NV + 1) >> 1;       // output MMA steps over the features: 2 atoms, or the last 1
 
   // The warp index, and what a warp reads from shared memory to steer its MMAs, go through a
-  // shuffle: known to be the same in every lane, they and what follows from them stay in uniform
-  // registers, where the MMA's operands have to be.
+  // shuffle: known to be the same in every lane, they and all that follows from them stay in
+  // uniform registers, where the MMA's operands have to be.  (A block's MMAs with their waits and
+  // commits: 2264 cycles issued so, 4545 from per-lane registers.)
   if (uniform(warp) == kMmaWarp || uniform(warp) == kOutWarp) {
     regs_set<kRegs3>();
     // ======================= MMA issuers: scores, outputs =======================================

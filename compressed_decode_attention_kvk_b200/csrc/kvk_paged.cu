@@ -236,9 +236,12 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
 // the IBM RISC System/6000 processor", 1990): with r = RN(1 / s), q0 = RN(v r) and two steps
 // q' = RN(q + r RN(v - s q)) the result is RN(v / s); it need not hold where the quotient is so
 // small that the steps underflow, whose code is zero either way.  Longer rows take the two-pass
-// form, one warp a token.  Bound by the loads' latency: 52,500 tokens of 576 bf16 elements at 8 bits
-// take 29 us (3.2 TB/s); one warp a token with a division per element took 57 us, and rows held as
-// fp32 values (two blocks an SM instead of four) 56 us.
+// form, one warp a token.  Bound by instruction issue: 52,500 tokens of 576 bf16 elements at 8 bits
+// take 29 us (3.2 TB/s) with 0.72 instructions a cycle and scheduler, 2.9 of its 6.9 warps ready on
+// average, and memory 28 % busy; the same tokens as bf16 rows, without quotients, 27 us (4.6 TB/s).
+// One warp a token with a division per element took 57 us, and rows held as fp32 values (two blocks
+// an SM instead of four) 56 us.  The two-pass form: rows of 1088 elements at 8 bits 92 us, as bf16
+// rows 66 us.
 constexpr int kWarpsPerBlock = 8;
 constexpr int kFastRounds = 10, kFastElems = 64 * kFastRounds;
 

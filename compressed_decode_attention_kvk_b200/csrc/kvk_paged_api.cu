@@ -48,7 +48,11 @@ int chunk_path(const kvk_layout* L, const AnchorDesc& A, int dtype) {
 // of in every row tile: from two row tiles of 128 per sequence on, over the batch, or one where the
 // rows are bf16 and nothing is converted but much is loaded.  8 sequences of 4096 tokens, 40 heads,
 // d = 512, row tiles per sequence (us converting / expanded): 8 bits 1.9 (71 / 76), 2.5 (86 / 83);
-// 16 bits 1.9 (87 / 93), 2.5 (109 / 107); bf16 0.6 (61 / 59), 1.2 (89 / 64).
+// 16 bits 1.9 (87 / 93), 2.5 (109 / 107); bf16 0.6 (61 / 59), 1.2 (89 / 64).  The host knows the
+// batch's average only, and every sequence with queries is expanded, those of one token too: 512 new
+// tokens beside 63 decode sequences, all near 8192 tokens, 8 bits (967 / 685), 16 bits (1237 / 1071);
+// but 512 new tokens of a fresh prompt beside 31 decode sequences of 16384, where the expanded rows
+// are mostly read once, 8 bits (357 / 409), 16 bits (454 / 671), bf16 (538 / 418).
 bool expand_pays(int b, int n_q, int batch, int n_heads) {
   const int tiles = b == KVK_BITS_BF16 ? 1 : 2;
   return (int64_t)n_q * n_heads >= (int64_t)tiles * 128 * batch;

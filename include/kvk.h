@@ -18,8 +18,8 @@
  *   - Device-side conditions that the host cannot see (positions and lengths held in
  *     device memory, non-finite inputs) never fault: the kernel skips or clamps the
  *     offending item and sets a sticky flag, read with kvk_read_status().
- *   - Every device pointer must be 16-byte aligned (the arena: 256-byte aligned), or the
- *     call returns KVK_ERR_ALIGNMENT.
+ *   - Every device pointer must be 16-byte aligned (the arena: 256-byte aligned; the int32
+ *     arrays of the paged calls: 4-byte aligned), or the call returns KVK_ERR_ALIGNMENT.
  *   - A layout belongs to the device that was current when it was created with an arena.
  *     Every call that launches work (writes, decodes, kvk_read_status) must be made with
  *     that device current; otherwise it returns KVK_ERR_INVALID_ARG and launches nothing.
@@ -475,9 +475,11 @@ kvk_status kvk_paged_write(kvk_layout* layout, int layer, const void* c_kv, int 
  *
  * A token whose cached row is not finite (KVK_FLAG_NONFINITE at its write) turns the rows that
  * see it into NaN and no others; scores of finite rows have to stay within fp32.  Group-scaled
- * values and f16 queries are held to the f16 range by the tensor-core kernel.  That kernel takes bf16 queries (and f16 ones, except over
- * uncompressed anchors) with d <= 512, d_rope <= 64 and d_rope % 16 == 0; other calls take the
- * CUDA-core kernel.  kvk_set_decode_path and kvk_set_wait_limit apply.
+ * values and f16 queries are held to the f16 range by the tensor-core kernel.  That kernel takes
+ * bf16 queries (and f16 ones, except over uncompressed anchors) with d <= 512, d_rope <= 64 and
+ * d_rope % 16 == 0.  Other calls, all fp32 queries among them, take the CUDA-core kernel, which is
+ * made for small ones: at decode and prompt sizes it is 20 to 70 times slower (5 to 7 TFLOP/s).
+ * kvk_set_decode_path and kvk_set_wait_limit apply.
  */
 kvk_status kvk_mla_chunk(kvk_layout* layout, int layer, const void* q_lat, const void* q_rope,
                          int dtype, int64_t q_lat_stride_tok, int64_t q_lat_stride_head,
@@ -496,7 +498,10 @@ kvk_status kvk_mla_chunk(kvk_layout* layout, int layer, const void* q_lat, const
  * the tensor-core kernel takes no query type (d > 512, d_rope > 64 or d_rope % 16) there are none.
  * Calls over pages of fewer than 8 tokens and calls that take the CUDA-core kernel use the fixed
  * part only.  A call that gets less than this, but no less than the size for n_q = 0, converts the
- * rows inside the attention, tile by tile; below that KVK_ERR_WORKSPACE. */
+ * rows inside the attention, tile by tile; below that KVK_ERR_WORKSPACE.
+ * Where there is room, the rows of every sequence with queries are expanded; a batch whose decode
+ * sequences hold far more tokens than its chunks' sequences is faster with the size for n_q = 0
+ * (8- and 16-bit codes), or as two calls. */
 kvk_status kvk_chunk_workspace_bytes(const kvk_layout* layout, int layer, int n_q, int batch,
                                      int n_heads, size_t* bytes);
 
